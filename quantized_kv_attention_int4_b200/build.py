@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libflashloop_b200.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = ["api.cu", "encode.cu", "dense.cu", "dense_staged.cu", "sparse.cu", "sparse_staged.cu", "sparse_persist.cu", "select.cu", "tokens.cu", "prefill.cu"]
+SOURCES = ["api.cu", "encode.cu", "dense.cu", "dense_staged.cu", "sparse.cu", "sparse_staged.cu", "sparse_persist.cu", "select.cu", "tokens.cu", "prefill.cu",
+           "paged_api.cu", "paged_index.cu", "paged_write.cu", "paged_attn.cu", "paged_select.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -28,7 +29,7 @@ def nvcc() -> str:
 
 
 def _newest_source_mtime() -> float:
-    paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "flashloop.h")]
+    paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return max(os.path.getmtime(p) for p in paths)
 
 

@@ -1,0 +1,277 @@
+// New tokens into the paged cache, and cached tokens back as BF16 rows
+// (include/flashloop_paged.h: fl_paged_append, fl_paged_read).
+#include "paged.cuh"
+#include "quant.cuh"
+
+namespace fl {
+namespace {
+
+// ---- append -----------------------------------------------------------------------------
+// An item is one block of one request that fills up (or, for a request none of whose blocks
+// fills up, its tail alone), for one head.  The item of a request's first block also writes
+// its new tail rows: that block is the only one whose older rows lie in the tail, so the CTA
+// has them in registers before it overwrites any.
+//
+// 256 threads: thread t owns channels 8 (t % 16) .. + 7 of rows t / 16 + 16 i, i = 0..3, of
+// keys and values (16-byte loads, 256-byte rows).  A value group (row, 64-channel half) is
+// eight neighbouring threads: three shuffles.  A key group (channel) is 64 rows: four in the
+// thread, two row sets in the warp, eight warps through shared memory.  Minima and maxima are
+// taken on the BF16 values, exact.
+constexpr int kAT = 256;
+
+struct AppendSmem {
+  uint32_t mn[8][64], mx[8][64];  // per warp and channel pair
+  uint32_t sz[kD];
+  int red[kAT / 32];
+};
+
+__device__ __forceinline__ uint32_t bmin2(uint32_t a, uint32_t b) {
+  __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
+  __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+
+// quant() of quant.cuh with its rounded division taken only near a half: with r = 1 / s
+// rounded, |d r - d / s| <= 1.6e-6 d / s < 3.2e-5 for codes up to 16 (beyond, both clamp), and
+// the rounded quotient is within 2^-20 of d / s, so away from a half by 1e-4 all of them
+// round to the same code.
+__device__ __forceinline__ uint32_t quant_fast(float x, float s, float r, float z) {
+  const float d = __fsub_rn(x, z), t = d * r, n = rintf(t);
+  if (fabsf(t - n) < 0.4999f) return (uint32_t)min(max(__float2int_rn(n), 0), 15);
+  return quant(x, s, z);
+}
+
+__device__ __forceinline__ uint32_t quant_word(uint4 x, const float2* sz, const float* rcp) {
+  float f[8];
+  bf16x8(x, f);
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w |= quant_fast(f[e], sz[e].x, rcp[e], sz[e].y) << (4 * e);
+  return w;
+}
+
+// 1 / s, and 0 for s = 0 (whose code is 0).
+__device__ __forceinline__ float rcp_scale(float s) { return s == 0.f ? 0.f : __frcp_rn(s); }
+
+__global__ void __launch_bounds__(kAT, 4) append_kernel(PagedAppendArgs a) {
+  extern __shared__ int32_t prefix[];
+  __shared__ AppendSmem sm;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int heads = a.p.kv_heads;
+  const fl_paged_index& x = a.x;
+  const bool tell = blockIdx.x == 0;
+  const int items = paged_scan<kAT>(a.batch, prefix, sm.red, [&](int b) {
+    const int s = paged_slot(x, a.slots, b, tell);
+    const int c = __ldg(a.start + b), r0 = __ldg(a.cu + b), r1 = __ldg(a.cu + b + 1);
+    if (s < 0 || c < 0 || r1 == r0) return 0;
+    if (r0 < 0 || r1 < r0 || r1 > a.n_tokens) {
+      if (tell) paged_error(x, FL_DEV_COUNT, b);
+      return 0;
+    }
+    if ((int64_t)c + (r1 - r0) > (int64_t)x.max_pages * FL_PAGE) {
+      if (tell) paged_error(x, FL_DEV_TOO_LONG, b);
+      return 0;
+    }
+    return max(1, paged_full(c + r1 - r0) - paged_full(c));
+  });
+  const int chunk = tid & 15, r0 = tid >> 4;
+  for (int64_t w = blockIdx.x; w < (int64_t)items * heads; w += gridDim.x) {
+    const int item = (int)(w / heads), h = (int)(w % heads);
+    const int b = paged_find(prefix, a.batch, item), j = item - prefix[b];
+    const int s = paged_slot(x, a.slots, b, false);
+    const int c = __ldg(a.start + b), row0 = __ldg(a.cu + b), n = c + __ldg(a.cu + b + 1) - row0;
+    const int full0 = paged_full(c), full1 = paged_full(n), block = full0 + j;
+    const size_t tail = ((size_t)s * heads + h) * FL_PAGE * kD;
+    uint16_t *tk = a.p.tail_k + tail, *tv = a.p.tail_v + tail;
+    int page = -1;
+    uint4 k4[4], v4[4];
+    if (block < full1) {
+      page = x.table[(int64_t)s * x.max_pages + block];
+      if (page < 0 || page >= x.pages) {
+        if (tid == 0) paged_error(x, FL_DEV_PAGE_RANGE, b);
+        page = -1;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = r0 + 16 * i, t = block * FL_PAGE + row;
+        const uint16_t *ks, *vs;
+        if (t < c) {
+          ks = tk + row * kD;
+          vs = tv + row * kD;
+        } else {
+          const int64_t off = (int64_t)(row0 + t - c) * a.token_stride + (int64_t)h * a.head_stride;
+          ks = a.k + off;
+          vs = a.v + off;
+        }
+        k4[i] = *reinterpret_cast<const uint4*>(ks + 8 * chunk);
+        v4[i] = *reinterpret_cast<const uint4*>(vs + 8 * chunk);
+      }
+    }
+    if (page >= 0) {
+      uint8_t* rec = a.p.rec + ((size_t)page * heads + h) * kRec;
+      // keys: this thread's four rows, the warp's other row set, then the eight warps
+      uint32_t mn[4], mx[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t p0 = (&k4[0].x)[e], p1 = (&k4[1].x)[e], p2 = (&k4[2].x)[e], p3 = (&k4[3].x)[e];
+        mn[e] = bmin2(bmin2(p0, p1), bmin2(p2, p3));
+        mx[e] = bmax2(bmax2(p0, p1), bmax2(p2, p3));
+        mn[e] = bmin2(mn[e], __shfl_xor_sync(kFull, mn[e], 16));
+        mx[e] = bmax2(mx[e], __shfl_xor_sync(kFull, mx[e], 16));
+      }
+      if (lane < 16) {
+        *reinterpret_cast<uint4*>(&sm.mn[warp][4 * chunk]) = make_uint4(mn[0], mn[1], mn[2], mn[3]);
+        *reinterpret_cast<uint4*>(&sm.mx[warp][4 * chunk]) = make_uint4(mx[0], mx[1], mx[2], mx[3]);
+      }
+      __syncthreads();
+      if (tid < kD) {
+        const int p = tid >> 1, sh = (tid & 1) * 16;
+        uint32_t lo = sm.mn[0][p], hi = sm.mx[0][p];
+#pragma unroll
+        for (int q = 1; q < 8; ++q) {
+          lo = bmin2(lo, sm.mn[q][p]);
+          hi = bmax2(hi, sm.mx[q][p]);
+        }
+        __half hs, hz;
+        group_sz(__uint_as_float((lo >> sh) << 16), __uint_as_float((hi >> sh) << 16), hs, hz);
+        sm.sz[tid] = pack_sz(hs, hz);
+        reinterpret_cast<uint32_t*>(rec + kRecKsz)[tid] = pack_sz(hs, hz);
+      }
+      __syncthreads();
+      {
+        const uint4 s0 = *reinterpret_cast<const uint4*>(&sm.sz[8 * chunk]);
+        const uint4 s1 = *reinterpret_cast<const uint4*>(&sm.sz[8 * chunk + 4]);
+        const float2 sz[8] = {unpack_sz(s0.x), unpack_sz(s0.y), unpack_sz(s0.z), unpack_sz(s0.w),
+                              unpack_sz(s1.x), unpack_sz(s1.y), unpack_sz(s1.z), unpack_sz(s1.w)};
+        float rcp[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) rcp[e] = rcp_scale(sz[e].x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint32_t*>(rec + (r0 + 16 * i) * 128 + 4 * chunk) = quant_word(k4[i], sz, rcp);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t lo = bmin2(bmin2(v4[i].x, v4[i].y), bmin2(v4[i].z, v4[i].w));
+        uint32_t hi = bmax2(bmax2(v4[i].x, v4[i].y), bmax2(v4[i].z, v4[i].w));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          lo = bmin2(lo, __shfl_xor_sync(kFull, lo, o));
+          hi = bmax2(hi, __shfl_xor_sync(kFull, hi, o));
+        }
+        __half hs, hz;
+        group_sz(fminf(bf16_lo(lo), bf16_hi(lo)), fmaxf(bf16_lo(hi), bf16_hi(hi)), hs, hz);
+        const int row = r0 + 16 * i;
+        if ((chunk & 7) == 0)
+          reinterpret_cast<uint32_t*>(rec + kRecVsz)[2 * row + (chunk >> 3)] = pack_sz(hs, hz);
+        const float sv = __half2float(hs), zv = __half2float(hz), rv = rcp_scale(sv);
+        const float2 sz[8] = {{sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}};
+        const float rcp[8] = {rv, rv, rv, rv, rv, rv, rv, rv};
+        *reinterpret_cast<uint32_t*>(rec + row * 128 + 64 + 4 * chunk) = quant_word(v4[i], sz, rcp);
+      }
+    }
+    __syncthreads();  // every old tail row is in registers (and sm is free again)
+    if (j == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = r0 + 16 * i, t = full1 * FL_PAGE + row;
+        if (t >= c && t < n) {
+          const int64_t off = (int64_t)(row0 + t - c) * a.token_stride + (int64_t)h * a.head_stride + 8 * chunk;
+          *reinterpret_cast<uint4*>(tk + row * kD + 8 * chunk) = *reinterpret_cast<const uint4*>(a.k + off);
+          *reinterpret_cast<uint4*>(tv + row * kD + 8 * chunk) = *reinterpret_cast<const uint4*>(a.v + off);
+        }
+      }
+    }
+  }
+}
+
+// ---- read -------------------------------------------------------------------------------
+// One warp takes 16 consecutive rows of one head: lane l owns channels 8 (l % 16) .. + 7 of
+// rows l / 16, l / 16 + 2, ...; the key scales of its channels stay in registers while the
+// page does not change.
+constexpr int kReadRows = 16, kReadWarps = 8;
+
+__device__ __forceinline__ uint32_t bf2(float a, float b) {
+  __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+// nibble e of w as an exact float
+__device__ __forceinline__ float nib(uint32_t w, int e) {
+  return __uint_as_float(((w >> (4 * e)) & 15u) | 0x4B000000u) - 8388608.f;
+}
+
+__global__ void __launch_bounds__(kReadWarps * 32) read_kernel(PagedReadArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int heads = a.p.kv_heads;
+  const int64_t job = (int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
+  const int64_t run = job / heads;
+  const int h = (int)(job % heads), t0 = (int)(run * kReadRows);
+  if (run * kReadRows >= a.n_tokens) return;
+  const int cl = lane & 15, half = lane >> 4;
+  const int mine = lane < kReadRows && t0 + lane < a.n_tokens ? __ldg(a.place + t0 + lane) : -1;
+  const int page_end = a.x.pages, all_end = a.x.pages + a.x.slots;
+  int cur = -1;
+  float2 ksz[8];
+#pragma unroll
+  for (int i = 0; i < kReadRows / 2; ++i) {
+    const int at = __shfl_sync(kFull, mine, 2 * i + half);
+    const int page = at >> 6, row = at & 63;
+    if (at < 0 || page >= all_end) {
+      if (h == 0 && cl == 0 && (at < -1 || page >= all_end)) paged_error(a.x, FL_DEV_PAGE_RANGE, t0 + 2 * i + half);
+      continue;
+    }
+    uint4 ko, vo;
+    if (page < page_end) {
+      const uint8_t* rec = a.p.rec + ((size_t)page * heads + h) * kRec;
+      const uint32_t kw = __ldg(reinterpret_cast<const uint32_t*>(rec + row * 128) + cl);
+      const uint32_t vw = __ldg(reinterpret_cast<const uint32_t*>(rec + row * 128 + 64) + cl);
+      const float2 vsz = unpack_sz(__ldg(reinterpret_cast<const uint32_t*>(rec + kRecVsz) + 2 * row + (cl >> 3)));
+      if (page != cur) {
+        const uint4 s0 = ldg_u4(rec + kRecKsz + 32 * cl), s1 = ldg_u4(rec + kRecKsz + 32 * cl + 16);
+        const uint32_t w[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ksz[e] = unpack_sz(w[e]);
+        cur = page;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        (&ko.x)[e] = bf2(fmaf(nib(kw, 2 * e), ksz[2 * e].x, ksz[2 * e].y), fmaf(nib(kw, 2 * e + 1), ksz[2 * e + 1].x, ksz[2 * e + 1].y));
+        (&vo.x)[e] = bf2(fmaf(nib(vw, 2 * e), vsz.x, vsz.y), fmaf(nib(vw, 2 * e + 1), vsz.x, vsz.y));
+      }
+    } else {
+      const size_t off = (((size_t)(page - page_end) * heads + h) * FL_PAGE + row) * kD + 8 * cl;
+      ko = ldg_u4(a.p.tail_k + off);
+      vo = ldg_u4(a.p.tail_v + off);
+    }
+    const int64_t off = (int64_t)(t0 + 2 * i + half) * a.token_stride + (int64_t)h * a.head_stride + 8 * cl;
+    *reinterpret_cast<uint4*>(a.k + off) = ko;
+    *reinterpret_cast<uint4*>(a.v + off) = vo;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
+  if (a.batch == 0 || a.n_tokens == 0) return cudaSuccess;
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  // at most one item per entry and one more per 64 tokens
+  const int64_t items = ((int64_t)a.batch + a.n_tokens / FL_PAGE) * a.p.kv_heads;
+  const int grid = (int)(items < 4 * sms ? items : 4 * sms);
+  append_kernel<<<grid, kAT, (size_t)(a.batch + 1) * 4, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_read(const PagedReadArgs& a, cudaStream_t s) {
+  if (a.n_tokens == 0) return cudaSuccess;
+  const int64_t jobs = ((int64_t)a.n_tokens + kReadRows - 1) / kReadRows * a.p.kv_heads;
+  const int64_t grid = (jobs + kReadWarps - 1) / kReadWarps;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  read_kernel<<<(unsigned)grid, kReadWarps * 32, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace fl
