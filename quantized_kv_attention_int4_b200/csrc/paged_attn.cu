@@ -1,128 +1,866 @@
 // Attention of one token per request over the paged cache (include/flashloop_paged.h:
 // fl_paged_attn_decode), over every block or over selected ones.
 //
-// One CTA per (entry, key-value head, eight query heads); a warp takes one token at a time,
-// lane l its channels 4l .. 4l + 3, with a running maximum and sum per query head; the warps'
-// states are joined in shared memory at the end.
+// Work.  A segment is one (entry, key-value head, up to 8 query heads of its group); its units
+// are its blocks (one 9216-byte record each) and its tail in quarters of 16 BF16 rows (8192
+// bytes), so a unit is about the same bytes whatever it is.  The units of all segments stand
+// in one line; each CTA takes an equal stretch of it and each warp an equal part of that, so
+// a batch of any mix of lengths keeps every SM equally busy and no length ever goes to the
+// host.  A segment that lies inside a warp's part is finished by the warp; the states (max,
+// sum, output) of one that several warps share are joined in shared memory, and of one that
+// several CTAs share by the last of them to arrive, always in the same order.
+//
+// Inside a warp.  Lane 0 brings the next unit with one TMA copy (128-byte swizzle) into one
+// of the warp's two or three stages while the warp computes on another: no warp waits for
+// another before the end.  Matrix products are warp-wide m16n8k16 with tokens (keys) or channels
+// (values) in the 16 rows and the query heads in the 8 columns: with 1 to 8 heads there is
+// nothing for a 64-row tcgen05 tile, whose operands would also have to be widened to 16 bits
+// in shared memory first.
+//
+//   q.k = sum_c (q_c s_c) (n_c - 8) + sum_c q_c (z_c + 8 s_c) for nibbles n.  A nibble under
+//   the exponent of 1024 is the binary16 number 1024 + n (1024 + 16 n at bits 4..7), so one
+//   logic and one packed fp16 operation turn two codes into two operands n - 8, exactly.  q_c
+//   has 8 significant bits and s_c 11, so q_c s_c is two binary16 parts exactly: hi = fl(q s),
+//   lo = fma(q, s, -hi); they fill columns 2j and 2j + 1 of query head j.  Powers of two keep
+//   both in range: q is scaled per head, s per record.  The second sum is one more product
+//   whose 16 rows are all z, and then all 8.
+//   o_c = sum_t (p_t s_t) (n_tc - 8) + sum_t p_t (z_t + 8 s_t) per 64-channel half.  p s goes
+//   in two binary16 parts as well (2^-22 relative), the second sum in fp32.
+//   The matrix unit's fp32 sums are cut off, not rounded: codes taken from the middle of
+//   their range keep partial sums small (with 0..15, whose products and zero points cancel,
+//   outputs over 8000 tokens were off by 1.7e-4), and a block's sums are added to the running
+//   ones in ordinary fp32.
+//   The running maximum is raised only when a score passes it by 8 (base 2): sums stay far
+//   inside fp32 and the accumulators are hardly ever rescaled.
+//   Tail rows are BF16: q.k exactly so, p in three BF16 parts (2^-24).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "paged.cuh"
 
 namespace fl {
 namespace {
 
-constexpr int kAW = 8;
+constexpr int kMaxCtas = 160;
+constexpr int kPart = 132;         // floats of a head's state: o[128], max, sum, -, -
+constexpr int kTailUnit = 16;      // tail rows of a unit
+constexpr int kTailBytes = 2 * kTailUnit * kD * 2;
 
-__global__ void __launch_bounds__(kAW * 32) paged_attn_kernel(PagedAttnArgs a) {
-  __shared__ float s_o[kAW][8][kD];
-  __shared__ float s_m[kAW][8], s_l[kAW][8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int chunks = (a.group + 7) / 8, heads = a.p.kv_heads;
-  const int b = blockIdx.y, h = blockIdx.x / chunks, g0 = blockIdx.x % chunks * 8;
-  const int gn = min(8, a.group - g0);
-  const fl_paged_index& x = a.x;
-  const bool tell = blockIdx.x == 0 && threadIdx.x == 0;
-  const int s = paged_slot(x, a.slots, b, tell);
-  if (s < 0) return;
-  const int n = paged_length(x, s, b, tell), full = paged_full(n);
-  const int nb = a.sel ? a.keep : full;
-  float q[8][4], acc[8][4], m[8], l[8];
+// Query heads of a segment: 4 kTiles.  Warps and stages: what registers (168 a thread for three
+// warps of a quarter of an SM, 255 for two) and shared memory allow.
+template <int kTiles>
+struct Shape {
+  static constexpr int kHeads = 4 * kTiles;
+  static constexpr int kWarps = kTiles == 1 ? 12 : 8;
+  static constexpr int kDepth = kTiles == 1 ? 2 : 3;  // stages of a warp
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kStages = kWarps * kDepth * kRec;
+  static constexpr int kSmem = 1024 + kStages;
+};
+
+// ---- instructions ---------------------------------------------------------------------
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], unsigned addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], unsigned addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void tma_rows(void* dst, const CUtensorMap* map, int row, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_addr(dst)),
+      "l"(map), "r"(0), "r"(row), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(unsigned addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(unsigned addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ __half2 h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+__device__ __forceinline__ uint32_t u2(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+// (a, b) rounded to a pair, a in the low half
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) { return u2(__floats2half2_rn(a, b)); }
+__device__ __forceinline__ uint32_t pack_b16(float a, float b) {
+  __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+// x in two binary16 parts, hi in the low half
+__device__ __forceinline__ uint32_t split_f16(float x) {
+  const float hi = __half2float(__float2half_rn(x));
+  return pack_f16(x, x - hi);
+}
+
+// ---- where a warp stands in the line of units --------------------------------------------
+struct Cursor {
+  int b, seg, u;       // entry, segment of the entry, unit of the segment
+  int units, np;       // units of a segment; the first np of them are blocks
+  int n, slot;
+  int64_t pages_at;    // table row, or -1 - (row of sel) once the segment is known
+};
+
+template <bool kSel>
+struct Line {
+  const PagedAttnArgs& a;
+  int chunks;
+
+  __device__ __forceinline__ int np_of(int n) const {
+    const int full = paged_full(n);
+    return kSel ? min(full, a.keep) : full;
+  }
+  // Units of a segment of entry b (0: padded).  A request of no tokens has one unit, empty.
+  __device__ __forceinline__ int units_of(int b, bool tell) const {
+    const int s = paged_slot(a.x, a.slots, b, tell);
+    if (s < 0) return 0;
+    const int n = paged_length(a.x, s, b, tell);
+    return n == 0 ? 1 : np_of(n) + (n - FL_PAGE * paged_full(n) + kTailUnit - 1) / kTailUnit;
+  }
+  // Entry b's lengths, or of the first entry from b on that has units.
+  __device__ __forceinline__ void enter(Cursor& c, int b) const {
+    for (; b < a.batch; ++b) {
+      c.slot = paged_slot(a.x, a.slots, b, false);
+      if (c.slot >= 0) break;
+    }
+    c.b = b;
+    if (b >= a.batch) return;
+    c.n = paged_length(a.x, c.slot, b, false);
+    c.np = np_of(c.n);
+    c.units = c.n == 0 ? 1 : c.np + (c.n - FL_PAGE * paged_full(c.n) + kTailUnit - 1) / kTailUnit;
+  }
+  __device__ __forceinline__ void next(Cursor& c) const {
+    if (++c.u < c.units) return;
+    c.u = 0;
+    if (++c.seg < a.p.kv_heads * chunks) return;
+    c.seg = 0;
+    enter(c, c.b + 1);
+  }
+};
+
+// The state of a segment's query heads in one warp.  Lane (i = lane / 4, j = lane % 4): its
+// accumulators' rows are channels, columns 2j, 2j + 1 the two parts of head j of each tile.
+template <int kTiles>
+struct State {
+  float acc[8][kTiles][4];  // [2 q + f]: rows i: channel 32 q + 4 i + 2 f, rows i + 8: the next
+  float m[kTiles], l[kTiles], z0[kTiles], z1[kTiles];  // max (all lanes of a head), this lane's sums
+
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    m[g] = -INFINITY;
-    l[g] = 0.f;
-    const uint16_t* src = a.q + (int64_t)b * a.q_batch_stride + (int64_t)(h * a.group + g0 + (g < gn ? g : 0)) * a.q_head_stride;
+    for (int t = 0; t < kTiles; ++t) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      q[g][c] = __uint_as_float((uint32_t)src[4 * lane + c] << 16);
-      acc[g][c] = 0.f;
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[k][t][c] = 0.f;
+      m[t] = -INFINITY;
+      l[t] = z0[t] = z1[t] = 0.f;
     }
   }
-  auto token = [&](const float* k, const float* v) {
+  // Raise the maxima to cover the unit's (top[t]: this lane's highest score of its head).
+  __device__ __forceinline__ void raise(const float (&top)[kTiles]) {
+    bool over = false;
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      if (g < gn) {
-        const float d = fmaf(q[g][0], k[0], fmaf(q[g][1], k[1], fmaf(q[g][2], k[2], q[g][3] * k[3])));
-        const float sc = warp_sum(d) * kQScale;
-        const float mn = fmaxf(m[g], sc), alpha = m[g] == -INFINITY ? 0.f : ex2(m[g] - mn), p = ex2(sc - mn);
-        m[g] = mn;
-        l[g] = fmaf(l[g], alpha, p);
+    for (int t = 0; t < kTiles; ++t) over |= top[t] > m[t] + 8.f;
+    if (!__any_sync(kFull, over)) return;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[g][c] = fmaf(acc[g][c], alpha, p * v[c]);
+    for (int t = 0; t < kTiles; ++t) {
+      float x = top[t];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+      const float mn = fmaxf(m[t], x), f = mn == m[t] ? 1.f : ex2(m[t] - mn);
+      m[t] = mn;
+      l[t] *= f;
+      z0[t] *= f;
+      z1[t] *= f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[k][t][c] *= f;
+    }
+  }
+};
+
+// Nibbles 0 and 4 of x (kOdd: 1 and 5) less 8, as a pair of binary16 numbers.
+template <bool kOdd>
+__device__ __forceinline__ uint32_t centred(uint32_t x) {
+  if constexpr (kOdd)
+    return u2(__hfma2(h2((x & 0x00f000f0u) | 0x64006400u), h2(0x2c002c00u), h2(0xd480d480u)));  // / 16 - 72
+  else
+    return u2(__hadd2(h2((x & 0x000f000fu) | 0x64006400u), h2(0xe408e408u)));  // - 1032
+}
+
+// The queries of a segment: lane (i, j) holds, for column i of each tile (head i / 2, part i
+// % 2), channels 32 q + 8 j + {0, 4}, {1, 5}, {2, 6}, {3, 7} scaled to [2^5, 2^6) at most.
+template <int kTiles>
+struct Query {
+  uint32_t w[kTiles][16];  // [4 q + pair]
+  float scale[kTiles];     // of head j (not i / 2): scores in base 2 = scaled dot times this
+  uint32_t part;           // all ones in the lanes of part 1
+
+  __device__ __forceinline__ void load(const PagedAttnArgs& a, int b, int head0, int live) {
+    const int lane = threadIdx.x & 31, i = lane >> 2, j = lane & 3;
+    part = i & 1 ? 0xffffffffu : 0u;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      const int g = 4 * t + (i >> 1);
+      uint4 x[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        x[q] = g < live ? ldg_u4(a.q + (int64_t)b * a.q_batch_stride + (int64_t)(head0 + g) * a.q_head_stride + 32 * q + 8 * j)
+                        : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t top = 0;  // largest magnitude's bits, in the high half
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t v = (&x[q].x)[c];
+          top = max(top, max((v << 16) & 0x7fffffffu, v & 0x7fff0000u));
+        }
+      top = max(top, __shfl_xor_sync(kFull, top, 1));
+      top = max(top, __shfl_xor_sync(kFull, top, 2));
+      // up = 2^(5 - floor(log2 top)), capped at 2^126; its reciprocal is exact
+      const int up = top == 0 ? 0 : min(5 - ((int)(top >> 23) - 127), 126);
+      const float f = pow2i(up), back = up > 120 ? pow2i(-60) * pow2i(60 - up) : pow2i(-up);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float v[8];
+        v[0] = bf16_lo(x[q].x) * f, v[1] = bf16_hi(x[q].x) * f, v[2] = bf16_lo(x[q].y) * f, v[3] = bf16_hi(x[q].y) * f;
+        v[4] = bf16_lo(x[q].z) * f, v[5] = bf16_hi(x[q].z) * f, v[6] = bf16_lo(x[q].w) * f, v[7] = bf16_hi(x[q].w) * f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[t][4 * q + c] = pack_f16(v[c], v[c + 4]);
+      }
+      scale[t] = __shfl_sync(kFull, back, 8 * j) * kQScale;
+    }
+  }
+};
+
+// One record in shared memory (swizzled rows of 128 bytes).
+template <int kTiles>
+__device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr, State<kTiles>& s) {
+  const int lane = threadIdx.x & 31, i = lane >> 2, j = lane & 3;
+  // largest key and value scales: 4 words a lane, scales in the low halves
+  const uint4 kw = lds128(st + (68 + (lane >> 3)) * 128 + (((lane & 7) ^ (4 + (lane >> 3))) << 4));
+  const uint4 vw = lds128(st + (64 + (lane >> 3)) * 128 + (((lane & 7) ^ (lane >> 3)) << 4));
+  const uint32_t ktop = __reduce_max_sync(kFull, max(max(kw.x << 16, kw.y << 16), max(kw.z << 16, kw.w << 16)));
+  const uint32_t vtop = __reduce_max_sync(kFull, max(max(vw.x << 16, vw.y << 16), max(vw.z << 16, vw.w << 16)));
+  // keys' scales times 2^(23 - ek): the largest in [2^8, 2^9); 8 in those units is 2^(ek - 20)
+  const int ek = max((int)(ktop >> 26) & 31, 8);
+  const uint32_t up = (uint32_t)(38 - ek) * 0x04000400u, eight = (uint32_t)(ek - 5) * 0x04000400u;
+
+  // ---- scores: 64 tokens x 8 columns a tile, two chains of four products each
+  float c[4][kTiles][4], zc[kTiles][4];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) zc[t][k] = 0.f;
+  const unsigned krow = st + (lane & 7) * 128 + (lane >> 3) * 1024;  // token 8 (lane / 8) + lane % 8
+#pragma unroll
+  for (int hq = 0; hq < 2; ++hq) {
+    float d[4][kTiles][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[r][t][k] = 0.f;
+#pragma unroll
+    for (int q = 2 * hq; q < 2 * hq + 2; ++q) {
+      const unsigned zrow = st + (68 + q) * 128;
+      const uint4 w0 = lds128(zrow + (((2 * j) ^ (4 + q)) << 4)), w1 = lds128(zrow + (((2 * j + 1) ^ (4 + q)) << 4));
+      uint32_t sp[4], zp[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sp[k] = u2(__hmul2(h2(__byte_perm((&w0.x)[k], (&w1.x)[k], 0x5410)), h2(up)));
+        zp[k] = __byte_perm((&w0.x)[k], (&w1.x)[k], 0x7632);
+      }
+      uint32_t bq[kTiles][4];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __half2 qv = h2(qr.w[t][4 * q + k]), sv = h2(sp[k]);
+          const uint32_t hi = u2(__hmul2(qv, sv)) & qr.part;  // part 0: fl(q s); part 1: q s - fl(q s)
+          bq[t][k] = u2(__hfma2(qv, sv, __hneg2(h2(hi))));
+        }
+        // q z in the columns of part 0 alone, 8 q s in its two parts
+        const uint32_t np = ~qr.part;
+        mma_f16(zc[t], zp[0], zp[0], zp[1], zp[1], qr.w[t][4 * q] & np, qr.w[t][4 * q + 1] & np);
+        mma_f16(zc[t], eight, eight, eight, eight, bq[t][0], bq[t][1]);
+        mma_f16(zc[t], zp[2], zp[2], zp[3], zp[3], qr.w[t][4 * q + 2] & np, qr.w[t][4 * q + 3] & np);
+        mma_f16(zc[t], eight, eight, eight, eight, bq[t][2], bq[t][3]);
+      }
+#pragma unroll
+      for (int r2 = 0; r2 < 2; ++r2) {
+        uint32_t k4[4];
+        ldsm4(k4, krow + r2 * 4096 + ((q ^ (lane & 7)) << 4));
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t a0 = k4[2 * r], a1 = k4[2 * r + 1], b0 = a0 >> 8, b1 = a1 >> 8;
+          const uint32_t e0 = centred<false>(a0), e1 = centred<false>(a1), o0 = centred<true>(a0), o1 = centred<true>(a1);
+          const uint32_t e2 = centred<false>(b0), e3 = centred<false>(b1), o2 = centred<true>(b0), o3 = centred<true>(b1);
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
+            mma_f16(d[2 * r2 + r][t], e0, e1, o0, o1, bq[t][0], bq[t][1]);
+            mma_f16(d[2 * r2 + r][t], e2, e3, o2, o3, bq[t][2], bq[t][3]);
+          }
+        }
       }
     }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[r][t][k] = hq == 0 ? d[r][t][k] : c[r][t][k] + d[r][t][k];
+  }
+  // lane (i, j): tokens 16 r + i and 16 r + 8 + i of head j
+  float top[kTiles];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const float f = qr.scale[t] * pow2i(ek - 23), base = (zc[t][0] + zc[t][1]) * qr.scale[t];
+    top[t] = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      c[r][t][0] = fmaf(c[r][t][0] + c[r][t][1], f, base);
+      c[r][t][1] = fmaf(c[r][t][2] + c[r][t][3], f, base);
+      top[t] = fmaxf(top[t], fmaxf(c[r][t][0], c[r][t][1]));
+    }
+  }
+  s.raise(top);
+  // values' scales times 2^(21 - ev): the largest in [2^6, 2^7), so that p s < 2^15
+  const int ev = max((int)(vtop >> 26) & 31, 1);
+  const float pe = pow2i(21 - ev), back = pow2i(ev - 21);
+  uint32_t bv[kTiles][2][8];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int tt = i + 8 * k;
+      const uint2 sz = lds64(st + (64 + r) * 128 + (((tt >> 1) ^ r) << 4) + (tt & 1) * 8);
+      const float2 f0 = unpack_sz(sz.x), f1 = unpack_sz(sz.y);
+      const float c0 = fmaf(8.f, f0.x, f0.y), c1 = fmaf(8.f, f1.x, f1.y);
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        const float p = ex2(c[r][t][k] - s.m[t]);
+        s.l[t] += p;
+        s.z0[t] = fmaf(p, c0, s.z0[t]);
+        s.z1[t] = fmaf(p, c1, s.z1[t]);
+        const float w = p * pe;
+        bv[t][0][2 * r + k] = transpose8(split_f16(w * f0.x));
+        bv[t][1][2 * r + k] = transpose8(split_f16(w * f1.x));
+      }
+    }
+  const unsigned vrow = st + (lane & 7) * 128 + (lane >> 3) * 1024;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float d[2][kTiles][4];
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[f][t][k] = 0.f;
+#pragma unroll
+    for (int r2 = 0; r2 < 2; ++r2) {
+      uint32_t v4[4];  // 32 channels of tokens 32 r2 + 0..7, 8..15, 16..23, 24..31
+      ldsm4t(v4, vrow + r2 * 4096 + (((4 + q) ^ (lane & 7)) << 4));
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t a0 = v4[2 * r], a1 = v4[2 * r + 1], b0 = a0 >> 8, b1 = a1 >> 8;
+        const uint32_t e0 = centred<false>(a0), e1 = centred<false>(a1), o0 = centred<true>(a0), o1 = centred<true>(a1);
+        const uint32_t e2 = centred<false>(b0), e3 = centred<false>(b1), o2 = centred<true>(b0), o3 = centred<true>(b1);
+        const int at = 4 * r2 + 2 * r;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          mma_f16(d[0][t], e0, o0, e1, o1, bv[t][q >> 1][at], bv[t][q >> 1][at + 1]);
+          mma_f16(d[1][t], e2, o2, e3, o3, bv[t][q >> 1][at], bv[t][q >> 1][at + 1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s.acc[2 * q + f][t][k] = fmaf(d[f][t][k], back, s.acc[2 * q + f][t][k]);
+  }
+}
+
+// `live` tail rows (1..16) in shared memory: keys at st, values at st + 4096, row t in the
+// 128-byte rows 2 t and 2 t + 1.
+template <int kTiles>
+__device__ __forceinline__ void tail_unit(unsigned st, int live, const PagedAttnArgs& a, int b, int head0, int heads,
+                                          State<kTiles>& s) {
+  const int lane = threadIdx.x & 31, i = lane >> 2, j = lane & 3;
+  float c[kTiles][4];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[t][k] = 0.f;
+  const int tok = (lane & 7) + (lane & 8);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int cc = 2 * k + (lane >> 4), row = 2 * tok + (cc >> 3);
+    uint32_t k4[4];
+    ldsm4(k4, st + row * 128 + (((cc & 7) ^ (row & 7)) << 4));
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      const int g = 4 * t + (i >> 1);
+      uint32_t b0 = 0u, b1 = 0u;
+      if (g < heads && !(i & 1)) {
+        const uint16_t* q = a.q + (int64_t)b * a.q_batch_stride + (int64_t)(head0 + g) * a.q_head_stride + 16 * k + 2 * j;
+        b0 = ldg_u32(q);
+        b1 = ldg_u32(q + 8);
+      }
+      mma_bf16(c[t], k4[0], k4[1], k4[2], k4[3], b0, b1);
+    }
+  }
+  float top[kTiles];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    c[t][0] = i < live ? c[t][0] * kQScale : -INFINITY;
+    c[t][1] = i + 8 < live ? c[t][2] * kQScale : -INFINITY;
+    top[t] = fmaxf(c[t][0], c[t][1]);
+  }
+  s.raise(top);
+  uint32_t bv[kTiles][2][2];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      // rows behind the last: exactly 0, whatever their scores
+      const float p = i + 8 * k < live ? ex2(c[t][k] - s.m[t]) : 0.f;
+      s.l[t] += p;
+      const float hi = __bfloat162float(__float2bfloat16_rn(p)), r1 = p - hi;  // parts of 8 bits
+      const float mid = __bfloat162float(__float2bfloat16_rn(r1));
+      // the first product has half of the high part in both columns: an infinite value meets no 0
+      bv[t][0][k] = transpose8(pack_b16(0.5f * hi, 0.5f * hi));
+      bv[t][1][k] = transpose8(pack_b16(mid, r1 - mid));
+    }
+  // rows behind the last may hold anything: their values are taken as 0
+  const uint32_t m0 = (2 * j < live ? 0xffffu : 0u) | (2 * j + 1 < live ? 0xffff0000u : 0u);
+  const uint32_t m1 = (2 * j + 8 < live ? 0xffffu : 0u) | (2 * j + 9 < live ? 0xffff0000u : 0u);
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  // x with its infinities and NaN (exponent 255) taken as 0, for the products of the low parts
+  auto finite = [](uint32_t x) {
+    return x & (((x & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) | ((x & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u));
   };
-  for (int i = warp; i < nb * FL_PAGE; i += kAW) {
-    int block = i >> 6;
-    if (a.sel) {
-      const int e = block;
-      block = a.sel[((size_t)b * heads + h) * a.keep + e];
-      if (block < 0 || block >= full) {
-        if (block != -1 && lane == 0 && (i & 63) == 0) paged_error(x, FL_DEV_SEL_BLOCK, b);
-        continue;
+  auto low_parts = [&](float (&acc)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    __nv_bfloat162 n = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a0), zero);  // NaN where not finite
+    n = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&a1), zero, n);
+    n = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&a2), zero, n);
+    n = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&a3), zero, n);
+    if (__any_sync(kFull, (*reinterpret_cast<uint32_t*>(&n) & 0x7fff7fffu) != 0u)) {
+      a0 = finite(a0);
+      a1 = finite(a1);
+      a2 = finite(a2);
+      a3 = finite(a3);
+    }
+    mma_bf16(acc, a0, a1, a2, a3, b0, b1);
+  };
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint2 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int t = 2 * j + (k & 1) + 8 * (k >> 1), row = 2 * t + (q >> 1);
+      v[k] = lds64(st + 4096 + row * 128 + (((4 * (q & 1) + (i >> 1)) ^ (row & 7)) << 4) + 8 * (i & 1));
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const uint32_t x0 = f ? v[0].y : v[0].x, x1 = f ? v[1].y : v[1].x, x2 = f ? v[2].y : v[2].x, x3 = f ? v[3].y : v[3].x;
+      const uint32_t a0 = __byte_perm(x0, x1, 0x5410) & m0, a1 = __byte_perm(x0, x1, 0x7632) & m0;
+      const uint32_t a2 = __byte_perm(x2, x3, 0x5410) & m1, a3 = __byte_perm(x2, x3, 0x7632) & m1;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_bf16(d, a0, a1, a2, a3, bv[t][0][0], bv[t][0][1]);
+        low_parts(d, a0, a1, a2, a3, bv[t][1][0], bv[t][1][1]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s.acc[2 * q + f][t][k] += d[k];
       }
     }
-    const int page = x.table[(int64_t)s * x.max_pages + block], row = i & 63;
-    if (page < 0 || page >= x.pages) {
-      if (lane == 0 && row == 0) paged_error(x, FL_DEV_PAGE_RANGE, b);
-      continue;
-    }
-    const uint8_t* rec = a.p.rec + ((size_t)page * heads + h) * kRec;
-    const uint32_t kc = *reinterpret_cast<const uint16_t*>(rec + row * 128 + 2 * lane);
-    const uint32_t vc = *reinterpret_cast<const uint16_t*>(rec + row * 128 + 64 + 2 * lane);
-    const uint4 ks = ldg_u4(rec + kRecKsz + 16 * lane);
-    const float2 vs = unpack_sz(ldg_u32(rec + kRecVsz + 8 * row + 4 * (lane >> 4)));
-    float k[4], v[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float2 f = unpack_sz((&ks.x)[c]);
-      k[c] = fmaf((float)((kc >> (4 * c)) & 15u), f.x, f.y);
-      v[c] = fmaf((float)((vc >> (4 * c)) & 15u), vs.x, vs.y);
-    }
-    token(k, v);
   }
-  for (int row = warp; row < n - full * FL_PAGE; row += kAW) {
-    const size_t off = (((size_t)s * heads + h) * FL_PAGE + row) * kD + 4 * lane;
-    const uint2 kw = *reinterpret_cast<const uint2*>(a.p.tail_k + off), vw = *reinterpret_cast<const uint2*>(a.p.tail_v + off);
-    const float k[4] = {bf16_lo(kw.x), bf16_hi(kw.x), bf16_lo(kw.y), bf16_hi(kw.y)};
-    const float v[4] = {bf16_lo(vw.x), bf16_hi(vw.x), bf16_lo(vw.y), bf16_hi(vw.y)};
-    token(k, v);
+}
+
+// Where a segment stands: its stretch of the line, its entry and heads.
+struct Segment {
+  int begin, end, b, seg;
+};
+
+__device__ __forceinline__ void write_head(const PagedAttnArgs& a, int b, int head, int at, float4 o, float m, float l,
+                                           bool lse) {
+  // l = 0: nothing was attended to
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<float4*>(a.o + (int64_t)b * a.o_batch_stride + (int64_t)head * a.o_head_stride + at) =
+      make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  if (lse && a.lse) a.lse[(size_t)b * a.q_heads + head] = l == 0.f ? -INFINITY : m + log2f(l);
+}
+
+// Loads of states: those of other CTAs (kL2) from L2, those of this CTA, in shared or global
+// memory, by their generic address.
+template <bool kL2, class T>
+__device__ __forceinline__ T ld_part(const T* p) {
+  if constexpr (kL2) return __ldcg(p);
+  else return *p;
+}
+
+// Join n states of one head (the k-th at part(k)): lane l takes channels 4 l .. 4 l + 3.
+template <bool kL2, class F>
+__device__ __forceinline__ void join(int n, F&& part, float4& o, float& m, float& l) {
+  const int lane = threadIdx.x & 31;
+  float top = -INFINITY;
+  for (int k = lane; k < n; k += 32) top = fmaxf(top, ld_part<kL2>(part(k) + kD));
+  m = warp_max(top);
+  l = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float* p = part(k);
+    const float2 ml = ld_part<kL2>(reinterpret_cast<const float2*>(p + kD));
+    const float4 x = ld_part<kL2>(reinterpret_cast<const float4*>(p) + lane);
+    const float f = ml.x == m ? 1.f : ex2(ml.x - m);  // also where no state has a maximum
+    l = fmaf(f, ml.y, l);
+    o.x = fmaf(f, x.x, o.x);
+    o.y = fmaf(f, x.y, o.y);
+    o.z = fmaf(f, x.z, o.z);
+    o.w = fmaf(f, x.w, o.w);
   }
+}
+
+template <int kTiles, bool kSel>
+__global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
+    paged_attn_kernel(const PagedAttnArgs a, const __grid_constant__ CUtensorMap map_rec,
+                      const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, int min_units) {
+  using Sh = Shape<kTiles>;
+  extern __shared__ uint8_t raw[];
+  __shared__ alignas(8) uint64_t bars[Sh::kWarps][Sh::kDepth];
+  __shared__ int red[Sh::kWarps];
+  uint8_t* stages = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int heads = a.p.kv_heads, chunks = (a.group + Sh::kHeads - 1) / Sh::kHeads;
+  const Line<kSel> line{a, chunks};
+
+  if (lane == 0) {
+    for (int d = 0; d < Sh::kDepth; ++d) mbar_init(&bars[warp][d], 1);
+    fence_mbar_init();
+  }
+  // the line of units, then this CTA's and this warp's stretch of it
+  int32_t* prefix = reinterpret_cast<int32_t*>(stages);
+  const bool tell = blockIdx.x == 0;
+  const int total = paged_scan<Sh::kThreads>(a.batch, prefix, red, [&](int b) { return line.units_of(b, tell) * heads * chunks; });
+  if (total == 0) return;
+  const int ctas = min((int)gridDim.x, max(total / min_units, 1));
+  if ((int)blockIdx.x >= ctas) return;
+  auto cta_begin = [&](int c) { return (int)((int64_t)total * c / ctas); };
+  const int clo = cta_begin(blockIdx.x), chi = cta_begin(blockIdx.x + 1);
+  // (with fewer units than warps the last warps have none)
+  auto warp_begin = [&](int w) {
+    return chi - clo >= Sh::kWarps ? clo + (int)((int64_t)(chi - clo) * w / Sh::kWarps) : min(clo + w, chi);
+  };
+  const int wlo = warp_begin(warp), whi = warp_begin(warp + 1);
+  Cursor use{};
+  int left = 0;  // units of the entry before this warp's first one
+  if (wlo < whi) {
+    const int b = paged_find(prefix, a.batch, wlo);
+    left = wlo - prefix[b];
+    use.b = b;
+  }
+  __syncthreads();  // the stages take over from the prefix sums
+  fence_proxy_async();
+
+  // states of pieces: the last one of a warp in its own stages, one before it in the workspace
+  float* parts = static_cast<float*>(a.data);
+  float* warp_parts = parts + (size_t)(blockIdx.x * Sh::kWarps) * Sh::kHeads * kPart;
+  float* cta_parts = parts + (size_t)kMaxCtas * Sh::kWarps * Sh::kHeads * kPart;
+  auto smem_part = [&](int w) { return reinterpret_cast<float*>(stages + (size_t)w * Sh::kDepth * kRec); };
+  auto global_part = [&](int w) { return warp_parts + (size_t)w * Sh::kHeads * kPart; };
+
+  Segment own[2];
+  int n_own = 0;
+  if (wlo < whi) {
+    line.enter(use, use.b);
+    use.seg = left / use.units;
+    use.u = left % use.units;
+    Cursor load = use;
+    int ids = -1, ids_b = -1, ids_seg = -1, ids_at = 0;  // lane l: page of unit ids_at + l of a segment
+    const unsigned st0 = smem_addr(stages) + warp * Sh::kDepth * kRec;
+    int issued = 0, in = 0;  // units issued, and the stage of the next one
+    int kinds[Sh::kDepth];   // of the units in flight: 0 nothing, -1 a block, else tail rows
+    auto issue = [&]() {
+      int kind = 0;
+      uint64_t* bar = &bars[warp][in];
+      uint8_t* dst = stages + (size_t)(warp * Sh::kDepth + in) * kRec;
+      const int h = load.seg / chunks;
+      if (load.u < load.np) {
+        if (load.b != ids_b || load.seg != ids_seg || load.u >= ids_at + 32) {
+          ids_b = load.b;
+          ids_seg = load.seg;
+          ids_at = load.u;
+          ids = -1;
+          if (load.u + lane < load.np) {
+            int block = load.u + lane;
+            bool ok = true;
+            if (kSel) {
+              block = __ldg(a.sel + ((size_t)load.b * heads + h) * a.keep + block);
+              ok = block >= 0 && block < paged_full(load.n);
+              if (!ok && block != -1 && load.seg % chunks == 0) paged_error(a.x, FL_DEV_SEL_BLOCK, load.b);
+            }
+            if (ok) {
+              ids = __ldg(a.x.table + (int64_t)load.slot * a.x.max_pages + block);
+              if (ids < 0 || ids >= a.x.pages) {
+                if (load.seg % chunks == 0) paged_error(a.x, FL_DEV_PAGE_RANGE, load.b);
+                ids = -1;
+              }
+            }
+          }
+        }
+        const int page = __shfl_sync(kFull, ids, load.u - ids_at);
+        if (page >= 0) {
+          kind = -1;
+          if (lane == 0) {
+            mbar_expect_tx(bar, kRec);
+            tma_rows(dst, &map_rec, (page * heads + h) * (kRec / 128), bar);
+          }
+        }
+      } else if (load.n > 0) {
+        const int row0 = (load.u - load.np) * kTailUnit;
+        kind = min(kTailUnit, load.n - FL_PAGE * paged_full(load.n) - row0);
+        if (lane == 0) {
+          mbar_expect_tx(bar, kTailBytes);
+          const int row = (load.slot * heads + h) * (2 * FL_PAGE) + 2 * row0;
+          tma_rows(dst, &map_k, row, bar);
+          tma_rows(dst + kTailBytes / 2, &map_v, row, bar);
+        }
+      }
+      if (kind == 0 && lane == 0) mbar_arrive(bar);
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
+      for (int d = 0; d < Sh::kDepth; ++d)
+        if (d == in) kinds[d] = kind;
+      in = in + 1 == Sh::kDepth ? 0 : in + 1;
+      ++issued;
+      line.next(load);
+    };
+    const int count = whi - wlo;
+    for (int d = 0; d < Sh::kDepth && d < count; ++d) issue();
+    int out = 0, phase = 0;  // the stage of the next unit to use, and its barrier's parity
+
+    State<kTiles> s;
+    Query<kTiles> qr;
+    int pos = wlo;
+    for (int k = 0; k < count;) {
+      const Segment seg{pos - use.u, pos - use.u + use.units, use.b, use.seg};
+      const int piece = min(use.units - use.u, whi - pos);
+      const int head0 = use.seg / chunks * a.group + use.seg % chunks * Sh::kHeads;
+      const int live = min(Sh::kHeads, a.group - use.seg % chunks * Sh::kHeads);
+      const bool whole = piece == use.units;
+      qr.load(a, use.b, head0, live);
+      s.clear();
+      for (int x = 0; x < piece; ++x, ++k) {
+        if (!mbar_wait(&bars[warp][out], phase)) {
+          if (lane == 0) paged_error(a.x, FL_DEV_TIMEOUT, use.b);
+          for (int d = 1; d < issued - k; ++d) {  // copies still in flight
+            out = out + 1 == Sh::kDepth ? 0 : out + 1;
+            if (out == 0) phase ^= 1;
+            mbar_wait(&bars[warp][out], phase);
+          }
+          k = count;
+          break;
+        }
+        const unsigned st = st0 + out * kRec;
+        int kind = kinds[0];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) s_o[warp][g][4 * lane + c] = acc[g][c];
-    if (lane == 0) {
-      s_m[warp][g] = m[g];
-      s_l[warp][g] = l[g];
+        for (int d = 1; d < Sh::kDepth; ++d)
+          if (d == out) kind = kinds[d];
+        out = out + 1 == Sh::kDepth ? 0 : out + 1;
+        if (out == 0) phase ^= 1;
+        if (kind < 0) block_unit<kTiles>(st, qr, s);
+        else if (kind > 0) tail_unit<kTiles>(st, kind, a, use.b, head0, live, s);
+        __syncwarp();
+        if (issued < count) issue();
+        line.next(use);
+      }
+      // this lane's channels of head j: 32 q + 4 i .. + 3
+      const int i = lane >> 2, j = lane & 3;
+      pos += piece;
+      float* part = pos == whi ? smem_part(warp) : global_part(warp);
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          s.l[t] += __shfl_xor_sync(kFull, s.l[t], o);
+          s.z0[t] += __shfl_xor_sync(kFull, s.z0[t], o);
+          s.z1[t] += __shfl_xor_sync(kFull, s.z1[t], o);
+        }
+        const int g = 4 * t + j;
+        if (g >= live) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float z = q < 2 ? s.z0[t] : s.z1[t];
+          float4 v;
+          v.x = s.acc[2 * q][t][0] + s.acc[2 * q][t][1] + z;
+          v.y = s.acc[2 * q][t][2] + s.acc[2 * q][t][3] + z;
+          v.z = s.acc[2 * q + 1][t][0] + s.acc[2 * q + 1][t][1] + z;
+          v.w = s.acc[2 * q + 1][t][2] + s.acc[2 * q + 1][t][3] + z;
+          if (whole) write_head(a, seg.b, head0 + g, 32 * q + 4 * i, v, s.m[t], s.l[t], q == 0 && i == 0);
+          else *reinterpret_cast<float4*>(part + g * kPart + 32 * q + 4 * i) = v;
+        }
+        if (!whole && i == 0) *reinterpret_cast<float2*>(part + g * kPart + kD) = make_float2(s.m[t], s.l[t]);
+      }
+      // the first piece of a segment in this CTA joins the others
+      if (!whole && pos - piece == max(seg.begin, clo)) {
+        own[n_own == 0 ? 0 : 1] = seg;
+        ++n_own;
+      }
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < gn * kD; i += kAW * 32) {
-    const int g = i / kD, c = i % kD;
-    float top = -INFINITY, sum = 0.f, o = 0.f;
-    bool nan = false;
-    for (int w = 0; w < kAW; ++w) {
-      top = fmaxf(top, s_m[w][g]);
-      nan |= s_l[w][g] != s_l[w][g];
+
+  for (int k = 0; k < n_own; ++k) {
+    const Segment seg = k == 0 ? own[0] : own[1];
+    // this warp and the next ones up to w1 hold its pieces
+    const int to = min(seg.end, chi);
+    int w1 = warp;
+    while (warp_begin(w1 + 1) < to) ++w1;
+    const bool first_moved = whi > seg.end;  // the segment ended inside this warp's part
+    const int c_head = seg.seg % chunks * Sh::kHeads;
+    const int head0 = seg.seg / chunks * a.group + c_head, live = min(Sh::kHeads, a.group - c_head);
+    const bool inside = seg.begin >= clo && seg.end <= chi;
+    const int c0 = (int)(((int64_t)(seg.begin + 1) * ctas - 1) / total), c1 = (int)(((int64_t)seg.end * ctas - 1) / total);
+    float* mine = cta_parts + (size_t)(2 * blockIdx.x + (seg.begin < clo ? 0 : 1)) * Sh::kHeads * kPart;
+    for (int g = 0; g < live; ++g) {
+      float4 o;
+      float m, l;
+      join<false>(w1 - warp + 1, [&](int x) -> const float* {
+        const int w = warp + x;
+        const bool last = x == 0 ? !first_moved : warp_begin(w + 1) <= seg.end;
+        return (last ? smem_part(w) : global_part(w)) + g * kPart;
+      }, o, m, l);
+      if (inside) {
+        write_head(a, seg.b, head0 + g, 4 * lane, o, m, l, lane == 0);
+      } else {
+        *(reinterpret_cast<float4*>(mine + g * kPart) + lane) = o;
+        if (lane == 0) *reinterpret_cast<float2*>(mine + g * kPart + kD) = make_float2(m, l);
+      }
     }
-    for (int w = 0; w < kAW; ++w) {
-      const float f = s_m[w][g] == -INFINITY && !nan ? 0.f : ex2(s_m[w][g] - top);
-      sum = fmaf(f, s_l[w][g], sum);
-      o = fmaf(f, s_o[w][g][c], o);
+    if (inside) continue;
+    // several CTAs share the segment: the last one to arrive joins their states
+    __threadfence();
+    __syncwarp();
+    int last = 0;
+    if (lane == 0) last = atomicAdd(&a.tickets[c0], 1) == c1 - c0;
+    last = __shfl_sync(kFull, last, 0);
+    if (!last) continue;
+    __threadfence();
+    if (lane == 0) a.tickets[c0] = 0;
+    for (int g = 0; g < live; ++g) {
+      float4 o;
+      float m, l;
+      join<true>(c1 - c0 + 1, [&](int x) -> const float* {
+        return cta_parts + ((size_t)(2 * (c0 + x) + (x == 0 ? 1 : 0)) * Sh::kHeads + g) * kPart;
+      }, o, m, l);
+      write_head(a, seg.b, head0 + g, 4 * lane, o, m, l, lane == 0);
     }
-    const int head = h * a.group + g0 + g;
-    a.o[(int64_t)b * a.o_batch_stride + (int64_t)head * a.o_head_stride + c] = n > 0 ? o / sum : 0.f;
-    if (c == 0 && a.lse) a.lse[(size_t)b * a.q_heads + head] = n > 0 ? top + log2f(sum) : -INFINITY;
   }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    return nullptr;
+  }();
+  return fn;
+}
+
+// `rows` rows of 128 bytes, copied `box` rows at a time with the 128-byte swizzle.
+bool rows_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {128, rows};
+  const cuuint64_t strides[1] = {128};
+  const cuuint32_t boxes[2] = {128, box};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, boxes, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+std::atomic<bool> g_attr_done[kMaxDevices];
+std::mutex g_attr_mu;
+
+template <int kTiles, bool kSel>
+cudaError_t launch(const PagedAttnArgs& a, int ctas, cudaStream_t s) {
+  using Sh = Shape<kTiles>;
+  CUtensorMap rec, tk, tv;
+  const uint64_t tail_rows = (uint64_t)a.x.slots * a.p.kv_heads * 2 * FL_PAGE;
+  if (!rows_map(&rec, a.p.rec, (uint64_t)a.x.pages * a.p.kv_heads * (kRec / 128), kRec / 128) ||
+      !rows_map(&tk, a.p.tail_k, tail_rows, 2 * kTailUnit) || !rows_map(&tv, a.p.tail_v, tail_rows, 2 * kTailUnit))
+    return cudaErrorInvalidValue;
+  paged_attn_kernel<kTiles, kSel><<<ctas, Sh::kThreads, Sh::kSmem, s>>>(a, rec, tk, tv, Sh::kWarps);
+  return cudaGetLastError();
+}
+
+template <int kTiles, bool kSel>
+cudaError_t allow_smem() {
+  return cudaFuncSetAttribute(paged_attn_kernel<kTiles, kSel>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<kTiles>::kSmem);
 }
 
 }  // namespace
 
-uint64_t paged_attn_bytes(const fl_paged_pool&, int) { return 0; }
+uint64_t paged_attn_bytes(const fl_paged_pool& p, int q_heads) {
+  const uint64_t heads = q_heads / p.kv_heads <= 4 ? 4 : 8, warps = heads == 4 ? Shape<1>::kWarps : Shape<2>::kWarps;
+  return (uint64_t)kMaxCtas * (warps + 2) * heads * kPart * sizeof(float);
+}
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
   if (a.batch == 0) return cudaSuccess;
-  paged_attn_kernel<<<dim3(a.p.kv_heads * ((a.group + 7) / 8), a.batch), kAW * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const cudaError_t e = once_per_device(g_attr_done, g_attr_mu, [](int) {
+    cudaError_t r = allow_smem<1, false>();
+    if (r == cudaSuccess) r = allow_smem<1, true>();
+    if (r == cudaSuccess) r = allow_smem<2, false>();
+    if (r == cudaSuccess) r = allow_smem<2, true>();
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  if (a.group <= 4) return a.sel ? launch<1, true>(a, ctas, s) : launch<1, false>(a, ctas, s);
+  return a.sel ? launch<2, true>(a, ctas, s) : launch<2, false>(a, ctas, s);
 }
 
 }  // namespace fl
