@@ -82,6 +82,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// d = a b
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -117,10 +124,11 @@ __device__ __forceinline__ uint32_t pack_b16(float a, float b) {
   __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&r);
 }
-// x in two binary16 parts, hi in the low half
+// x >= 0 in two binary16 parts, the first (its 11 leading bits, cut off) in the low half.  The
+// second is rounded, 2^-22 of x at most; below 2^-14 both lose bits under 2^-24.
 __device__ __forceinline__ uint32_t split_f16(float x) {
-  const float hi = __half2float(__float2half_rn(x));
-  return pack_f16(x, x - hi);
+  const float hi = __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+  return pack_f16(hi, x - hi);
 }
 
 // ---- where a warp stands in the line of units --------------------------------------------
@@ -210,13 +218,19 @@ struct State {
   }
 };
 
+// (x & mask) | magic in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t magic) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(mask), "r"(magic));
+  return y;
+}
 // Nibbles 0 and 4 of x (kOdd: 1 and 5) less 8, as a pair of binary16 numbers.
 template <bool kOdd>
 __device__ __forceinline__ uint32_t centred(uint32_t x) {
   if constexpr (kOdd)
-    return u2(__hfma2(h2((x & 0x00f000f0u) | 0x64006400u), h2(0x2c002c00u), h2(0xd480d480u)));  // / 16 - 72
+    return u2(__hfma2(h2(and_or(x, 0x00f000f0u, 0x64006400u)), h2(0x2c002c00u), h2(0xd480d480u)));  // / 16 - 72
   else
-    return u2(__hadd2(h2((x & 0x000f000fu) | 0x64006400u), h2(0xe408e408u)));  // - 1032
+    return u2(__hadd2(h2(and_or(x, 0x000f000fu, 0x64006400u)), h2(0xe408e408u)));  // - 1032
 }
 
 // The queries of a segment: lane (i, j) holds, for column i of each tile (head i / 2, part i
@@ -279,24 +293,16 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
 
   // ---- scores: 64 tokens x 8 columns a tile, two chains of four products each
   float c[4][kTiles][4], zc[kTiles][4];
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) zc[t][k] = 0.f;
-  const unsigned krow = st + (lane & 7) * 128 + (lane >> 3) * 1024;  // token 8 (lane / 8) + lane % 8
+  // stages start at multiples of 1024 bytes and the swizzle changes address bits 4..6 alone, so
+  // a chunk's place is one exclusive or away.  Row of token 8 (lane / 8) + lane % 8, its chunk 0:
+  const unsigned code0 = st + (lane & 7) * 128 + (lane >> 3) * 1024 + ((lane & 7) << 4);
+  const unsigned sz0 = st + 68 * 128 + (j << 5), vsz0 = st + 64 * 128 + ((i >> 1) << 4) + (i & 1) * 8;
 #pragma unroll
   for (int hq = 0; hq < 2; ++hq) {
     float d[4][kTiles][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) d[r][t][k] = 0.f;
-#pragma unroll
     for (int q = 2 * hq; q < 2 * hq + 2; ++q) {
-      const unsigned zrow = st + (68 + q) * 128;
-      const uint4 w0 = lds128(zrow + (((2 * j) ^ (4 + q)) << 4)), w1 = lds128(zrow + (((2 * j + 1) ^ (4 + q)) << 4));
+      const uint4 w0 = lds128((sz0 ^ ((4 + q) << 4)) + q * 128), w1 = lds128((sz0 ^ ((5 ^ q) << 4)) + q * 128);
       uint32_t sp[4], zp[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -314,7 +320,8 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
         }
         // q z in the columns of part 0 alone, 8 q s in its two parts
         const uint32_t np = ~qr.part;
-        mma_f16(zc[t], zp[0], zp[0], zp[1], zp[1], qr.w[t][4 * q] & np, qr.w[t][4 * q + 1] & np);
+        if (q == 0) mma_f16_first(zc[t], zp[0], zp[0], zp[1], zp[1], qr.w[t][4 * q] & np, qr.w[t][4 * q + 1] & np);
+        else mma_f16(zc[t], zp[0], zp[0], zp[1], zp[1], qr.w[t][4 * q] & np, qr.w[t][4 * q + 1] & np);
         mma_f16(zc[t], eight, eight, eight, eight, bq[t][0], bq[t][1]);
         mma_f16(zc[t], zp[2], zp[2], zp[3], zp[3], qr.w[t][4 * q + 2] & np, qr.w[t][4 * q + 3] & np);
         mma_f16(zc[t], eight, eight, eight, eight, bq[t][2], bq[t][3]);
@@ -322,7 +329,7 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
 #pragma unroll
       for (int r2 = 0; r2 < 2; ++r2) {
         uint32_t k4[4];
-        ldsm4(k4, krow + r2 * 4096 + ((q ^ (lane & 7)) << 4));
+        ldsm4(k4, (code0 ^ (q << 4)) + r2 * 4096);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const uint32_t a0 = k4[2 * r], a1 = k4[2 * r + 1], b0 = a0 >> 8, b1 = a1 >> 8;
@@ -330,7 +337,8 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
           const uint32_t e2 = centred<false>(b0), e3 = centred<false>(b1), o2 = centred<true>(b0), o3 = centred<true>(b1);
 #pragma unroll
           for (int t = 0; t < kTiles; ++t) {
-            mma_f16(d[2 * r2 + r][t], e0, e1, o0, o1, bq[t][0], bq[t][1]);
+            if (q == 2 * hq) mma_f16_first(d[2 * r2 + r][t], e0, e1, o0, o1, bq[t][0], bq[t][1]);
+            else mma_f16(d[2 * r2 + r][t], e0, e1, o0, o1, bq[t][0], bq[t][1]);
             mma_f16(d[2 * r2 + r][t], e2, e3, o2, o3, bq[t][2], bq[t][3]);
           }
         }
@@ -343,20 +351,24 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
 #pragma unroll
         for (int k = 0; k < 4; ++k) c[r][t][k] = hq == 0 ? d[r][t][k] : c[r][t][k] + d[r][t][k];
   }
-  // lane (i, j): tokens 16 r + i and 16 r + 8 + i of head j
-  float top[kTiles];
+  // lane (i, j): tokens 16 r + i and 16 r + 8 + i of head j; a score is sum f + base, f >= 0
+  float top[kTiles], f[kTiles], off[kTiles];
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
-    const float f = qr.scale[t] * pow2i(ek - 23), base = (zc[t][0] + zc[t][1]) * qr.scale[t];
-    top[t] = -INFINITY;
+    f[t] = qr.scale[t] * pow2i(ek - 23);
+    off[t] = (zc[t][0] + zc[t][1]) * qr.scale[t];
+    float mx = -INFINITY;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      c[r][t][0] = fmaf(c[r][t][0] + c[r][t][1], f, base);
-      c[r][t][1] = fmaf(c[r][t][2] + c[r][t][3], f, base);
-      top[t] = fmaxf(top[t], fmaxf(c[r][t][0], c[r][t][1]));
+      c[r][t][0] += c[r][t][1];
+      c[r][t][1] = c[r][t][2] + c[r][t][3];
+      mx = fmaxf(mx, fmaxf(c[r][t][0], c[r][t][1]));
     }
+    top[t] = fmaf(mx, f[t], off[t]);
   }
   s.raise(top);
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) off[t] -= s.m[t];
   // values' scales times 2^(21 - ev): the largest in [2^6, 2^7), so that p s < 2^15
   const int ev = max((int)(vtop >> 26) & 31, 1);
   const float pe = pow2i(21 - ev), back = pow2i(ev - 21);
@@ -365,13 +377,12 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
   for (int r = 0; r < 4; ++r)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int tt = i + 8 * k;
-      const uint2 sz = lds64(st + (64 + r) * 128 + (((tt >> 1) ^ r) << 4) + (tt & 1) * 8);
+      const uint2 sz = lds64((vsz0 ^ ((r ^ (4 * k)) << 4)) + r * 128);  // of token 16 r + 8 k + i
       const float2 f0 = unpack_sz(sz.x), f1 = unpack_sz(sz.y);
       const float c0 = fmaf(8.f, f0.x, f0.y), c1 = fmaf(8.f, f1.x, f1.y);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        const float p = ex2(c[r][t][k] - s.m[t]);
+        const float p = ex2(fmaf(c[r][t][k], f[t], off[t]));
         s.l[t] += p;
         s.z0[t] = fmaf(p, c0, s.z0[t]);
         s.z1[t] = fmaf(p, c1, s.z1[t]);
@@ -380,20 +391,13 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
         bv[t][1][2 * r + k] = transpose8(split_f16(w * f1.x));
       }
     }
-  const unsigned vrow = st + (lane & 7) * 128 + (lane >> 3) * 1024;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     float d[2][kTiles][4];
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) d[f][t][k] = 0.f;
-#pragma unroll
     for (int r2 = 0; r2 < 2; ++r2) {
       uint32_t v4[4];  // 32 channels of tokens 32 r2 + 0..7, 8..15, 16..23, 24..31
-      ldsm4t(v4, vrow + r2 * 4096 + (((4 + q) ^ (lane & 7)) << 4));
+      ldsm4t(v4, (code0 ^ ((4 + q) << 4)) + r2 * 4096);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const uint32_t a0 = v4[2 * r], a1 = v4[2 * r + 1], b0 = a0 >> 8, b1 = a1 >> 8;
@@ -402,8 +406,13 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
         const int at = 4 * r2 + 2 * r;
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
-          mma_f16(d[0][t], e0, o0, e1, o1, bv[t][q >> 1][at], bv[t][q >> 1][at + 1]);
-          mma_f16(d[1][t], e2, o2, e3, o3, bv[t][q >> 1][at], bv[t][q >> 1][at + 1]);
+          if (at == 0) {
+            mma_f16_first(d[0][t], e0, o0, e1, o1, bv[t][q >> 1][at], bv[t][q >> 1][at + 1]);
+            mma_f16_first(d[1][t], e2, o2, e3, o3, bv[t][q >> 1][at], bv[t][q >> 1][at + 1]);
+          } else {
+            mma_f16(d[0][t], e0, o0, e1, o1, bv[t][q >> 1][at], bv[t][q >> 1][at + 1]);
+            mma_f16(d[1][t], e2, o2, e3, o3, bv[t][q >> 1][at], bv[t][q >> 1][at + 1]);
+          }
         }
       }
     }
@@ -613,62 +622,58 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     use.seg = left / use.units;
     use.u = left % use.units;
     Cursor load = use;
-    int ids = -1, ids_b = -1, ids_seg = -1, ids_at = 0;  // lane l: page of unit ids_at + l of a segment
-    const unsigned st0 = smem_addr(stages) + warp * Sh::kDepth * kRec;
+    int rows = -1, rows_at = 0, rows_end = 0;  // lane l: record row of unit rows_at + l of the segment
+    uint8_t* const st0 = stages + (size_t)warp * Sh::kDepth * kRec;
     int issued = 0, in = 0;  // units issued, and the stage of the next one
-    int kinds[Sh::kDepth];   // of the units in flight: 0 nothing, -1 a block, else tail rows
+    unsigned voids = 0;      // stages whose block could not be read
     auto issue = [&]() {
-      int kind = 0;
       uint64_t* bar = &bars[warp][in];
-      uint8_t* dst = stages + (size_t)(warp * Sh::kDepth + in) * kRec;
-      const int h = load.seg / chunks;
+      uint8_t* dst = st0 + in * kRec;
+      const int h = chunks == 1 ? load.seg : load.seg / chunks;
       if (load.u < load.np) {
-        if (load.b != ids_b || load.seg != ids_seg || load.u >= ids_at + 32) {
-          ids_b = load.b;
-          ids_seg = load.seg;
-          ids_at = load.u;
-          ids = -1;
+        if (load.u >= rows_end) {
+          rows_at = load.u;
+          rows_end = min(load.u + 32, load.np);
+          rows = -1;
           if (load.u + lane < load.np) {
+            const bool told = load.seg % chunks == 0;
             int block = load.u + lane;
             bool ok = true;
             if (kSel) {
               block = __ldg(a.sel + ((size_t)load.b * heads + h) * a.keep + block);
               ok = block >= 0 && block < paged_full(load.n);
-              if (!ok && block != -1 && load.seg % chunks == 0) paged_error(a.x, FL_DEV_SEL_BLOCK, load.b);
+              if (!ok && block != -1 && told) paged_error(a.x, FL_DEV_SEL_BLOCK, load.b);
             }
             if (ok) {
-              ids = __ldg(a.x.table + (int64_t)load.slot * a.x.max_pages + block);
-              if (ids < 0 || ids >= a.x.pages) {
-                if (load.seg % chunks == 0) paged_error(a.x, FL_DEV_PAGE_RANGE, load.b);
-                ids = -1;
-              }
+              const int page = __ldg(a.x.table + (int64_t)load.slot * a.x.max_pages + block);
+              if (page >= 0 && page < a.x.pages) rows = (page * heads + h) * (kRec / 128);
+              else if (told) paged_error(a.x, FL_DEV_PAGE_RANGE, load.b);
             }
           }
         }
-        const int page = __shfl_sync(kFull, ids, load.u - ids_at);
-        if (page >= 0) {
-          kind = -1;
-          if (lane == 0) {
+        const int row = __shfl_sync(kFull, rows, load.u - rows_at);
+        if (lane == 0) {
+          if (row >= 0) {
             mbar_expect_tx(bar, kRec);
-            tma_rows(dst, &map_rec, (page * heads + h) * (kRec / 128), bar);
+            tma_rows(dst, &map_rec, row, bar);
+          } else {
+            mbar_arrive(bar);
           }
         }
-      } else if (load.n > 0) {
-        const int row0 = (load.u - load.np) * kTailUnit;
-        kind = min(kTailUnit, load.n - FL_PAGE * paged_full(load.n) - row0);
-        if (lane == 0) {
+        voids = (voids & ~(1u << in)) | ((unsigned)(row < 0) << in);
+      } else if (lane == 0) {
+        if (load.n > 0) {
           mbar_expect_tx(bar, kTailBytes);
-          const int row = (load.slot * heads + h) * (2 * FL_PAGE) + 2 * row0;
+          const int row = (load.slot * heads + h) * (2 * FL_PAGE) + 2 * kTailUnit * (load.u - load.np);
           tma_rows(dst, &map_k, row, bar);
           tma_rows(dst + kTailBytes / 2, &map_v, row, bar);
+        } else {
+          mbar_arrive(bar);
         }
       }
-      if (kind == 0 && lane == 0) mbar_arrive(bar);
-#pragma unroll
-      for (int d = 0; d < Sh::kDepth; ++d)
-        if (d == in) kinds[d] = kind;
       in = in + 1 == Sh::kDepth ? 0 : in + 1;
       ++issued;
+      if (load.u + 1 == load.units) rows_end = 0;
       line.next(load);
     };
     const int count = whi - wlo;
@@ -686,6 +691,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       const bool whole = piece == use.units;
       qr.load(a, use.b, head0, live);
       s.clear();
+      const int tail_rows = use.n - FL_PAGE * paged_full(use.n);
       for (int x = 0; x < piece; ++x, ++k) {
         if (!mbar_wait(&bars[warp][out], phase)) {
           if (lane == 0) paged_error(a.x, FL_DEV_TIMEOUT, use.b);
@@ -697,22 +703,23 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
           k = count;
           break;
         }
-        const unsigned st = st0 + out * kRec;
-        int kind = kinds[0];
-#pragma unroll
-        for (int d = 1; d < Sh::kDepth; ++d)
-          if (d == out) kind = kinds[d];
+        const unsigned st = smem_addr(st0) + out * kRec;
+        const int tail = use.u + x - use.np;  // quarter of the tail, negative for a block
+        if (tail >= 0) {
+          if (use.n > 0) tail_unit<kTiles>(st, min(kTailUnit, tail_rows - kTailUnit * tail), a, use.b, head0, live, s);
+        } else if (!((voids >> out) & 1u)) {
+          block_unit<kTiles>(st, qr, s);
+        }
         out = out + 1 == Sh::kDepth ? 0 : out + 1;
         if (out == 0) phase ^= 1;
-        if (kind < 0) block_unit<kTiles>(st, qr, s);
-        else if (kind > 0) tail_unit<kTiles>(st, kind, a, use.b, head0, live, s);
         __syncwarp();
         if (issued < count) issue();
-        line.next(use);
       }
       // this lane's channels of head j: 32 q + 4 i .. + 3
       const int i = lane >> 2, j = lane & 3;
       pos += piece;
+      use.u += piece - 1;
+      line.next(use);
       float* part = pos == whi ? smem_part(warp) : global_part(warp);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
