@@ -131,7 +131,7 @@ fl_status fl_paged_read(const fl_paged_index* index, const fl_paged_pool* pool, 
 /* Workspace of the two calls below for up to `batch` entries and q_heads query heads (0 for
  * arguments out of range).  fl_paged_workspace_init zeroes its first FL_PAGED_WS_HEAD bytes:
  * once before the first call, and again after FL_DEV_TIMEOUT. */
-#define FL_PAGED_WS_HEAD 4096
+#define FL_PAGED_WS_HEAD 8192
 size_t fl_paged_workspace_bytes(const fl_paged_index* index, const fl_paged_pool* pool, int32_t batch,
                                 int32_t q_heads);
 fl_status fl_paged_workspace_init(void* ws, size_t ws_bytes, void* stream);

@@ -23,7 +23,7 @@
 //   has 8 significant bits and s_c 11, so q_c s_c is two binary16 parts exactly: hi = fl(q s),
 //   lo = fma(q, s, -hi); they fill columns 2j and 2j + 1 of query head j.  Powers of two keep
 //   both in range: q is scaled per head, s per record.  The second sum is one more product
-//   whose 16 rows are all z, and then all 8.
+//   whose rows are all z, and then all 8.
 //   o_c = sum_t (p_t s_t) (n_tc - 8) + sum_t p_t (z_t + 8 s_t) per 64-channel half.  p s goes
 //   in two binary16 parts as well (2^-22 relative), the second sum in fp32.
 //   The matrix unit's fp32 sums are cut off, not rounded: codes taken from the middle of
@@ -102,6 +102,9 @@ __device__ __forceinline__ void tma_rows(void* dst, const CUtensorMap* map, int 
       "l"(map), "r"(0), "r"(row), "r"(smem_addr(bar))
       : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -133,46 +136,70 @@ __device__ __forceinline__ uint32_t split_f16(float x) {
 
 // ---- where a warp stands in the line of units --------------------------------------------
 struct Cursor {
-  int b, seg, u;       // entry, segment of the entry, unit of the segment
-  int units, np;       // units of a segment; the first np of them are blocks
+  int b, h, ch, u;  // entry, key-value head, which heads of its group, unit of the segment
+  int units, np;    // units of a segment; the first np of them are blocks
   int n, slot;
-  int64_t pages_at;    // table row, or -1 - (row of sel) once the segment is known
 };
 
-template <bool kSel>
+// Where a segment stands: its stretch of the line, its entry and heads.
+struct Segment {
+  int begin, end, b, h, ch;
+};
+
+template <int kHeads, bool kSel>
 struct Line {
   const PagedAttnArgs& a;
   int chunks;
 
-  __device__ __forceinline__ int np_of(int n) const {
+  __device__ __forceinline__ int blocks_of(int n) const {
     const int full = paged_full(n);
     return kSel ? min(full, a.keep) : full;
   }
-  // Units of a segment of entry b (0: padded).  A request of no tokens has one unit, empty.
-  __device__ __forceinline__ int units_of(int b, bool tell) const {
-    const int s = paged_slot(a.x, a.slots, b, tell);
-    if (s < 0) return 0;
-    const int n = paged_length(a.x, s, b, tell);
-    return n == 0 ? 1 : np_of(n) + (n - FL_PAGE * paged_full(n) + kTailUnit - 1) / kTailUnit;
+  // Units of a segment of n tokens; one of no tokens has one unit, empty.
+  __device__ __forceinline__ int units_of(int n) const {
+    return n == 0 ? 1 : blocks_of(n) + (n - FL_PAGE * paged_full(n) + kTailUnit - 1) / kTailUnit;
   }
-  // Entry b's lengths, or of the first entry from b on that has units.
-  __device__ __forceinline__ void enter(Cursor& c, int b) const {
-    for (; b < a.batch; ++b) {
-      c.slot = paged_slot(a.x, a.slots, b, false);
-      if (c.slot >= 0) break;
-    }
-    c.b = b;
-    if (b >= a.batch) return;
-    c.n = paged_length(a.x, c.slot, b, false);
-    c.np = np_of(c.n);
-    c.units = c.n == 0 ? 1 : c.np + (c.n - FL_PAGE * paged_full(c.n) + kTailUnit - 1) / kTailUnit;
+  __device__ __forceinline__ void place(Cursor& c, int n) const {
+    c.n = n;
+    c.np = blocks_of(n);
+    c.units = units_of(n);
   }
+  // The next unit; the entry behind the last one is a.batch.
   __device__ __forceinline__ void next(Cursor& c) const {
     if (++c.u < c.units) return;
     c.u = 0;
-    if (++c.seg < a.p.kv_heads * chunks) return;
-    c.seg = 0;
-    enter(c, c.b + 1);
+    if (++c.ch < chunks) return;
+    c.ch = 0;
+    if (++c.h < a.p.kv_heads) return;
+    c.h = 0;
+#pragma unroll 1
+    while (++c.b < a.batch) {
+      c.slot = paged_slot(a.x, a.slots, c.b, false);
+      if (c.slot < 0) continue;
+      place(c, paged_length(a.x, c.slot, c.b, false));
+      return;
+    }
+  }
+  // The first query head, and how many
+  __device__ __forceinline__ int head(int h, int ch) const { return h * a.group + ch * kHeads; }
+  __device__ __forceinline__ int live(int ch) const { return min(kHeads, a.group - ch * kHeads); }
+};
+
+// Errors of one lane, told at the kernel's end (one place of the code): the first one's code and
+// entry, and how many.
+struct Errors {
+  int first = 0, detail = 0, count = 0;
+
+  __device__ __forceinline__ void add(int code, int b) {
+    if (count++ == 0) {
+      first = code;
+      detail = b;
+    }
+  }
+  __device__ __forceinline__ void tell(const fl_paged_index& x) const {
+    if (count == 0 || !x.status) return;
+    record_error(x.status, first, detail);
+    if (count > 1) atomicAdd(&x.status[2], count - 1);
   }
 };
 
@@ -240,18 +267,26 @@ struct Query {
   uint32_t w[kTiles][16];  // [4 q + pair]
   float scale[kTiles];     // of head j (not i / 2): scores in base 2 = scaled dot times this
   uint32_t part;           // all ones in the lanes of part 1
+  uint4 raw[kTiles][4];    // as read
 
-  __device__ __forceinline__ void load(const PagedAttnArgs& a, int b, int head0, int live) {
+  // Start the loads; prepare() waits for them.
+  __device__ __forceinline__ void fetch(const PagedAttnArgs& a, int b, int head0, int live) {
+    const int lane = threadIdx.x & 31, i = lane >> 2, j = lane & 3;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      const int g = 4 * t + (i >> 1);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        raw[t][q] = g < live ? ldg_u4(a.q + (int64_t)b * a.q_batch_stride + (int64_t)(head0 + g) * a.q_head_stride + 32 * q + 8 * j)
+                             : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  __device__ __forceinline__ void prepare() {
     const int lane = threadIdx.x & 31, i = lane >> 2, j = lane & 3;
     part = i & 1 ? 0xffffffffu : 0u;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      const int g = 4 * t + (i >> 1);
-      uint4 x[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        x[q] = g < live ? ldg_u4(a.q + (int64_t)b * a.q_batch_stride + (int64_t)(head0 + g) * a.q_head_stride + 32 * q + 8 * j)
-                        : make_uint4(0u, 0u, 0u, 0u);
+      const uint4(&x)[4] = raw[t];
       uint32_t top = 0;  // largest magnitude's bits, in the high half
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -318,12 +353,11 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
           const uint32_t hi = u2(__hmul2(qv, sv)) & qr.part;  // part 0: fl(q s); part 1: q s - fl(q s)
           bq[t][k] = u2(__hfma2(qv, sv, __hneg2(h2(hi))));
         }
-        // q z in the columns of part 0 alone, 8 q s in its two parts
-        const uint32_t np = ~qr.part;
-        if (q == 0) mma_f16_first(zc[t], zp[0], zp[0], zp[1], zp[1], qr.w[t][4 * q] & np, qr.w[t][4 * q + 1] & np);
-        else mma_f16(zc[t], zp[0], zp[0], zp[1], zp[1], qr.w[t][4 * q] & np, qr.w[t][4 * q + 1] & np);
+        // rows 0..7: q z + 8 hi (and, unused, q z + 8 lo); rows 8..15: 8 hi (unused) and 8 lo
+        if (q == 0) mma_f16_first(zc[t], zp[0], 0u, zp[1], 0u, qr.w[t][4 * q], qr.w[t][4 * q + 1]);
+        else mma_f16(zc[t], zp[0], 0u, zp[1], 0u, qr.w[t][4 * q], qr.w[t][4 * q + 1]);
         mma_f16(zc[t], eight, eight, eight, eight, bq[t][0], bq[t][1]);
-        mma_f16(zc[t], zp[2], zp[2], zp[3], zp[3], qr.w[t][4 * q + 2] & np, qr.w[t][4 * q + 3] & np);
+        mma_f16(zc[t], zp[2], 0u, zp[3], 0u, qr.w[t][4 * q + 2], qr.w[t][4 * q + 3]);
         mma_f16(zc[t], eight, eight, eight, eight, bq[t][2], bq[t][3]);
       }
 #pragma unroll
@@ -356,7 +390,7 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
     f[t] = qr.scale[t] * pow2i(ek - 23);
-    off[t] = (zc[t][0] + zc[t][1]) * qr.scale[t];
+    off[t] = (zc[t][0] + zc[t][3]) * qr.scale[t];
     float mx = -INFINITY;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -426,39 +460,46 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
 }
 
 // `live` tail rows (1..16) in shared memory: keys at st, values at st + 4096, row t in the
-// 128-byte rows 2 t and 2 t + 1.
+// 128-byte rows 2 t and 2 t + 1.  The queries come from the registers block_unit's products
+// use, so channels go to the matrix unit in their order.
 template <int kTiles>
-__device__ __forceinline__ void tail_unit(unsigned st, int live, const PagedAttnArgs& a, int b, int head0, int heads,
-                                          State<kTiles>& s) {
+__device__ __forceinline__ void tail_unit(unsigned st, int live, const Query<kTiles>& qr, State<kTiles>& s) {
   const int lane = threadIdx.x & 31, i = lane >> 2, j = lane & 3;
   float c[kTiles][4];
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
     for (int k = 0; k < 4; ++k) c[t][k] = 0.f;
-  const int tok = (lane & 7) + (lane & 8);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int cc = 2 * k + (lane >> 4), row = 2 * tok + (cc >> 3);
-    uint32_t k4[4];
-    ldsm4(k4, st + row * 128 + (((cc & 7) ^ (row & 7)) << 4));
+  for (int q = 0; q < 4; ++q) {
+    // channels 32 q + 8 j .. + 7 of tokens i and i + 8, as the pairs {0, 4}, {1, 5}, {2, 6}, {3, 7}
+    uint32_t k4[2][4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int row = 2 * (i + 8 * x) + (q >> 1);
+      const uint4 v = lds128(st + row * 128 + (((4 * (q & 1) + j) ^ (row & 7)) << 4));
+      k4[x][0] = __byte_perm(v.x, v.z, 0x5410);
+      k4[x][1] = __byte_perm(v.x, v.z, 0x7632);
+      k4[x][2] = __byte_perm(v.y, v.w, 0x5410);
+      k4[x][3] = __byte_perm(v.y, v.w, 0x7632);
+    }
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      const int g = 4 * t + (i >> 1);
-      uint32_t b0 = 0u, b1 = 0u;
-      if (g < heads && !(i & 1)) {
-        const uint16_t* q = a.q + (int64_t)b * a.q_batch_stride + (int64_t)(head0 + g) * a.q_head_stride + 16 * k + 2 * j;
-        b0 = ldg_u32(q);
-        b1 = ldg_u32(q + 8);
+      uint32_t b[4];  // the query in BF16, exact, in the columns of part 0
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = __half22float2(h2(qr.w[t][4 * q + k]));
+        b[k] = pack_b16(f.x, f.y) & ~qr.part;
       }
-      mma_bf16(c[t], k4[0], k4[1], k4[2], k4[3], b0, b1);
+      mma_bf16(c[t], k4[0][0], k4[1][0], k4[0][1], k4[1][1], b[0], b[1]);
+      mma_bf16(c[t], k4[0][2], k4[1][2], k4[0][3], k4[1][3], b[2], b[3]);
     }
   }
   float top[kTiles];
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
-    c[t][0] = i < live ? c[t][0] * kQScale : -INFINITY;
-    c[t][1] = i + 8 < live ? c[t][2] * kQScale : -INFINITY;
+    c[t][0] = i < live ? c[t][0] * qr.scale[t] : -INFINITY;
+    c[t][1] = i + 8 < live ? c[t][2] * qr.scale[t] : -INFINITY;
     top[t] = fmaxf(c[t][0], c[t][1]);
   }
   s.raise(top);
@@ -479,91 +520,115 @@ __device__ __forceinline__ void tail_unit(unsigned st, int live, const PagedAttn
   // rows behind the last may hold anything: their values are taken as 0
   const uint32_t m0 = (2 * j < live ? 0xffffu : 0u) | (2 * j + 1 < live ? 0xffff0000u : 0u);
   const uint32_t m1 = (2 * j + 8 < live ? 0xffffu : 0u) | (2 * j + 9 < live ? 0xffff0000u : 0u);
-  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
-  // x with its infinities and NaN (exponent 255) taken as 0, for the products of the low parts
-  auto finite = [](uint32_t x) {
-    return x & (((x & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) | ((x & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u));
-  };
-  auto low_parts = [&](float (&acc)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    __nv_bfloat162 n = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a0), zero);  // NaN where not finite
-    n = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&a1), zero, n);
-    n = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&a2), zero, n);
-    n = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&a3), zero, n);
-    if (__any_sync(kFull, (*reinterpret_cast<uint32_t*>(&n) & 0x7fff7fffu) != 0u)) {
-      a0 = finite(a0);
-      a1 = finite(a1);
-      a2 = finite(a2);
-      a3 = finite(a3);
+  // the high part of p, then the low ones, for which infinities and NaN are taken as 0
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    uint32_t b[kTiles][2];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      b[t][0] = pass ? bv[t][1][0] : bv[t][0][0];
+      b[t][1] = pass ? bv[t][1][1] : bv[t][0][1];
     }
-    mma_bf16(acc, a0, a1, a2, a3, b0, b1);
-  };
+    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+    __nv_bfloat162 nan = zero;  // NaN once a value is not finite
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint2 v[4];
+    for (int q = 0; q < 4; ++q) {
+      uint2 v[4];  // channels 32 q + 4 i .. + 3 of tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int t = 2 * j + (k & 1) + 8 * (k >> 1), row = 2 * t + (q >> 1);
-      v[k] = lds64(st + 4096 + row * 128 + (((4 * (q & 1) + (i >> 1)) ^ (row & 7)) << 4) + 8 * (i & 1));
-    }
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const uint32_t x0 = f ? v[0].y : v[0].x, x1 = f ? v[1].y : v[1].x, x2 = f ? v[2].y : v[2].x, x3 = f ? v[3].y : v[3].x;
-      const uint32_t a0 = __byte_perm(x0, x1, 0x5410) & m0, a1 = __byte_perm(x0, x1, 0x7632) & m0;
-      const uint32_t a2 = __byte_perm(x2, x3, 0x5410) & m1, a3 = __byte_perm(x2, x3, 0x7632) & m1;
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_bf16(d, a0, a1, a2, a3, bv[t][0][0], bv[t][0][1]);
-        low_parts(d, a0, a1, a2, a3, bv[t][1][0], bv[t][1][1]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s.acc[2 * q + f][t][k] += d[k];
+      for (int k = 0; k < 4; ++k) {
+        const int t = 2 * j + (k & 1) + 8 * (k >> 1), row = 2 * t + (q >> 1);
+        v[k] = lds64(st + 4096 + row * 128 + (((4 * (q & 1) + (i >> 1)) ^ (row & 7)) << 4) + 8 * (i & 1));
       }
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const uint32_t x0 = f ? v[0].y : v[0].x, x1 = f ? v[1].y : v[1].x, x2 = f ? v[2].y : v[2].x, x3 = f ? v[3].y : v[3].x;
+        uint32_t av[4] = {__byte_perm(x0, x1, 0x5410) & m0, __byte_perm(x0, x1, 0x7632) & m0,
+                          __byte_perm(x2, x3, 0x5410) & m1, __byte_perm(x2, x3, 0x7632) & m1};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) nan = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&av[e]), zero, nan);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_bf16(d, av[0], av[1], av[2], av[3], b[t][0], b[t][1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s.acc[2 * q + f][t][e] += d[e];
+        }
+      }
+    }
+    if (pass == 0 && __any_sync(kFull, (*reinterpret_cast<uint32_t*>(&nan) & 0x7fff7fffu) != 0u)) {
+      // rare: the values that are not finite give way to 0 in place
+      __syncwarp();
+#pragma unroll 1
+      for (int w = lane; w < kTailBytes / 8; w += 32) {
+        const unsigned at = st + 4096 + 4 * w;
+        uint32_t x;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+        x &= ((x & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) | ((x & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+      }
+      fence_proxy_async();  // before the next copy into this stage
+      __syncwarp();
     }
   }
 }
 
-// Where a segment stands: its stretch of the line, its entry and heads.
-struct Segment {
-  int begin, end, b, seg;
-};
+// 1 / l, and 0 where nothing was attended to (l = 0); log2 of the sum of 2^score
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : __frcp_rn(l); }
+__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
 
-__device__ __forceinline__ void write_head(const PagedAttnArgs& a, int b, int head, int at, float4 o, float m, float l,
-                                           bool lse) {
-  // l = 0: nothing was attended to
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<float4*>(a.o + (int64_t)b * a.o_batch_stride + (int64_t)head * a.o_head_stride + at) =
-      make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  if (lse && a.lse) a.lse[(size_t)b * a.q_heads + head] = l == 0.f ? -INFINITY : m + log2f(l);
+// States lie in shared memory, or in global memory where another SM may have written them: read
+// by their generic address, past this SM's cache.
+__device__ __forceinline__ float2 ld_part2(const float* p) {
+  float2 v;
+  asm volatile("ld.relaxed.gpu.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_part4(const float* p) {
+  float4 v;
+  asm volatile("ld.relaxed.gpu.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+  return v;
 }
 
-// Loads of states: those of other CTAs (kL2) from L2, those of this CTA, in shared or global
-// memory, by their generic address.
-template <bool kL2, class T>
-__device__ __forceinline__ T ld_part(const T* p) {
-  if constexpr (kL2) return __ldcg(p);
-  else return *p;
-}
-
-// Join n states of one head (the k-th at part(k)): lane l takes channels 4 l .. 4 l + 3.
-template <bool kL2, class F>
+// Join n states of one head (the k-th at part(k)), 32 at a time: lane l weighs state l, then
+// takes channels 4 l .. 4 l + 3 of each.
+template <class F>
 __device__ __forceinline__ void join(int n, F&& part, float4& o, float& m, float& l) {
   const int lane = threadIdx.x & 31;
-  float top = -INFINITY;
-  for (int k = lane; k < n; k += 32) top = fmaxf(top, ld_part<kL2>(part(k) + kD));
-  m = warp_max(top);
+  m = -INFINITY;
   l = 0.f;
   o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float* p = part(k);
-    const float2 ml = ld_part<kL2>(reinterpret_cast<const float2*>(p + kD));
-    const float4 x = ld_part<kL2>(reinterpret_cast<const float4*>(p) + lane);
-    const float f = ml.x == m ? 1.f : ex2(ml.x - m);  // also where no state has a maximum
-    l = fmaf(f, ml.y, l);
-    o.x = fmaf(f, x.x, o.x);
-    o.y = fmaf(f, x.y, o.y);
-    o.z = fmaf(f, x.z, o.z);
-    o.w = fmaf(f, x.w, o.w);
+#pragma unroll 1
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    const float* p = part(min(k0 + lane, n - 1));
+    float2 ml = ld_part2(p + kD);
+    if (k0 + lane >= n) ml = make_float2(-INFINITY, 0.f);
+    const float top = fmaxf(m, warp_max(fmaxf(ml.x, -INFINITY)));
+    const float old = m == top ? 1.f : ex2(m - top);
+    const float f = k0 + lane >= n ? 0.f : ml.x == top ? 1.f : ex2(ml.x - top);  // 1 also where no state has a maximum
+    m = top;
+    l = fmaf(l, old, warp_sum(f * ml.y));
+    o.x *= old;
+    o.y *= old;
+    o.z *= old;
+    o.w *= old;
+    const int cnt = min(32, n - k0);
+#pragma unroll 1
+    for (int k = 0; k < cnt; k += 4) {  // (lanes from n on repeat the last state, with weight 0)
+      float4 x[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        x[y] = ld_part4(reinterpret_cast<const float*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(p), (k + y) & 31)) + 4 * lane);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float fk = __shfl_sync(kFull, f, (k + y) & 31);
+        if (k + y < cnt) {
+          o.x = fmaf(fk, x[y].x, o.x);
+          o.y = fmaf(fk, x[y].y, o.y);
+          o.z = fmaf(fk, x[y].z, o.z);
+          o.w = fmaf(fk, x[y].w, o.w);
+        }
+      }
+    }
   }
 }
 
@@ -575,35 +640,65 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
   extern __shared__ uint8_t raw[];
   __shared__ alignas(8) uint64_t bars[Sh::kWarps][Sh::kDepth];
   __shared__ int red[Sh::kWarps];
+  __shared__ Segment s_own[Sh::kWarps][2];  // segments whose first piece in this CTA a warp holds
+  __shared__ int s_owned[Sh::kWarps];
+  __shared__ int s_begin[Sh::kWarps + 1];       // the warps' stretches
+  __shared__ const float* s_first[Sh::kWarps];  // where the state of a warp's first piece is
   uint8_t* stages = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int heads = a.p.kv_heads, chunks = (a.group + Sh::kHeads - 1) / Sh::kHeads;
-  const Line<kSel> line{a, chunks};
+  const Line<Sh::kHeads, kSel> line{a, chunks};
+  Errors errors;
 
   if (lane == 0) {
     for (int d = 0; d < Sh::kDepth; ++d) mbar_init(&bars[warp][d], 1);
     fence_mbar_init();
+    if (warp == 0) {
+      prefetch_map(&map_rec);
+      prefetch_map(&map_k);
+      prefetch_map(&map_v);
+    }
   }
   // the line of units, then this CTA's and this warp's stretch of it
-  int32_t* prefix = reinterpret_cast<int32_t*>(stages);
-  const bool tell = blockIdx.x == 0;
-  const int total = paged_scan<Sh::kThreads>(a.batch, prefix, red, [&](int b) { return line.units_of(b, tell) * heads * chunks; });
-  if (total == 0) return;
+  int32_t* prefix = reinterpret_cast<int32_t*>(stages);  // [batch + 1]
+  int32_t* lengths = prefix + a.batch + 1;                // [batch]
+  const int total = paged_scan<Sh::kThreads>(a.batch, prefix, red, [&](int b) {
+    const int s = a.slots ? __ldg(a.slots + b) : b;
+    if (s < 0 || s >= a.x.slots) {
+      if (s != -1 && blockIdx.x == 0) errors.add(FL_DEV_SLOT_RANGE, b);
+      return 0;
+    }
+    int n = a.x.length[s];
+    if (n < 0 || n > a.x.max_pages * FL_PAGE) {
+      if (blockIdx.x == 0) errors.add(FL_DEV_TOO_LONG, b);
+      n = 0;
+    }
+    lengths[b] = n;
+    return line.units_of(n) * heads * chunks;
+  });
+  // a small call takes fewer CTAs: a warp should have a unit, and joins have their price
   const int ctas = min((int)gridDim.x, max(total / min_units, 1));
-  if ((int)blockIdx.x >= ctas) return;
-  auto cta_begin = [&](int c) { return (int)((int64_t)total * c / ctas); };
-  const int clo = cta_begin(blockIdx.x), chi = cta_begin(blockIdx.x + 1);
+  if ((int)blockIdx.x >= ctas || total == 0) {
+    errors.tell(a.x);
+    return;
+  }
+  const int clo = (int)((int64_t)total * blockIdx.x / ctas), chi = (int)((int64_t)total * (blockIdx.x + 1) / ctas);
   // (with fewer units than warps the last warps have none)
-  auto warp_begin = [&](int w) {
-    return chi - clo >= Sh::kWarps ? clo + (int)((int64_t)(chi - clo) * w / Sh::kWarps) : min(clo + w, chi);
-  };
-  const int wlo = warp_begin(warp), whi = warp_begin(warp + 1);
+  if (threadIdx.x <= Sh::kWarps)
+    s_begin[threadIdx.x] = chi - clo >= Sh::kWarps ? clo + (int)((unsigned)((chi - clo) / Sh::kWarps) * threadIdx.x +
+                                                                 (unsigned)((chi - clo) % Sh::kWarps) * threadIdx.x / Sh::kWarps)
+                                                   : min(clo + (int)threadIdx.x, chi);
+  __syncthreads();
+  const int wlo = s_begin[warp], whi = s_begin[warp + 1];
   Cursor use{};
-  int left = 0;  // units of the entry before this warp's first one
   if (wlo < whi) {
-    const int b = paged_find(prefix, a.batch, wlo);
-    left = wlo - prefix[b];
-    use.b = b;
+    use.b = paged_find(prefix, a.batch, wlo);
+    use.slot = a.slots ? __ldg(a.slots + use.b) : use.b;
+    line.place(use, lengths[use.b]);
+    const int left = wlo - prefix[use.b], seg = left / use.units;
+    use.u = left - seg * use.units;
+    use.h = chunks == 1 ? seg : seg / chunks;
+    use.ch = seg - use.h * chunks;
   }
   __syncthreads();  // the stages take over from the prefix sums
   fence_proxy_async();
@@ -615,86 +710,123 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
   auto smem_part = [&](int w) { return reinterpret_cast<float*>(stages + (size_t)w * Sh::kDepth * kRec); };
   auto global_part = [&](int w) { return warp_parts + (size_t)w * Sh::kHeads * kPart; };
 
-  Segment own[2];
   int n_own = 0;
   if (wlo < whi) {
-    line.enter(use, use.b);
-    use.seg = left / use.units;
-    use.u = left % use.units;
+    Query<kTiles> qr;
+    State<kTiles> s;
     Cursor load = use;
     int rows = -1, rows_at = 0, rows_end = 0;  // lane l: record row of unit rows_at + l of the segment
     uint8_t* const st0 = stages + (size_t)warp * Sh::kDepth * kRec;
     int issued = 0, in = 0;  // units issued, and the stage of the next one
     unsigned voids = 0;      // stages whose block could not be read
+    const int count = whi - wlo;
     auto issue = [&]() {
       uint64_t* bar = &bars[warp][in];
       uint8_t* dst = st0 + in * kRec;
-      const int h = chunks == 1 ? load.seg : load.seg / chunks;
+      voids &= ~(1u << in);
       if (load.u < load.np) {
         if (load.u >= rows_end) {
           rows_at = load.u;
           rows_end = min(load.u + 32, load.np);
           rows = -1;
-          if (load.u + lane < load.np) {
-            const bool told = load.seg % chunks == 0;
-            int block = load.u + lane;
-            bool ok = true;
-            if (kSel) {
-              block = __ldg(a.sel + ((size_t)load.b * heads + h) * a.keep + block);
-              ok = block >= 0 && block < paged_full(load.n);
-              if (!ok && block != -1 && told) paged_error(a.x, FL_DEV_SEL_BLOCK, load.b);
-            }
-            if (ok) {
+          int block = load.u + lane;
+          if (block < load.np) {
+            if (kSel) block = __ldg(a.sel + ((size_t)load.b * heads + load.h) * a.keep + block);
+            int error = 0;
+            if (!kSel || (block >= 0 && block < paged_full(load.n))) {
               const int page = __ldg(a.x.table + (int64_t)load.slot * a.x.max_pages + block);
-              if (page >= 0 && page < a.x.pages) rows = (page * heads + h) * (kRec / 128);
-              else if (told) paged_error(a.x, FL_DEV_PAGE_RANGE, load.b);
+              if (page >= 0 && page < a.x.pages) rows = (page * heads + load.h) * (kRec / 128);
+              else error = FL_DEV_PAGE_RANGE;
+            } else if (block != -1) {
+              error = FL_DEV_SEL_BLOCK;
             }
+            if (error && load.ch == 0) errors.add(error, load.b);
           }
         }
         const int row = __shfl_sync(kFull, rows, load.u - rows_at);
-        if (lane == 0) {
-          if (row >= 0) {
-            mbar_expect_tx(bar, kRec);
-            tma_rows(dst, &map_rec, row, bar);
-          } else {
-            mbar_arrive(bar);
-          }
+        if (row < 0) {
+          voids |= 1u << in;
+          if (lane == 0) mbar_arrive(bar);
+        } else if (lane == 0) {
+          mbar_expect_tx(bar, kRec);
+          tma_rows(dst, &map_rec, row, bar);
         }
-        voids = (voids & ~(1u << in)) | ((unsigned)(row < 0) << in);
+      } else if (load.n == 0) {
+        if (lane == 0) mbar_arrive(bar);
       } else if (lane == 0) {
-        if (load.n > 0) {
-          mbar_expect_tx(bar, kTailBytes);
-          const int row = (load.slot * heads + h) * (2 * FL_PAGE) + 2 * kTailUnit * (load.u - load.np);
-          tma_rows(dst, &map_k, row, bar);
-          tma_rows(dst + kTailBytes / 2, &map_v, row, bar);
-        } else {
-          mbar_arrive(bar);
-        }
+        mbar_expect_tx(bar, kTailBytes);
+        const int row = (load.slot * heads + load.h) * (2 * FL_PAGE) + 2 * kTailUnit * (load.u - load.np);
+        tma_rows(dst, &map_k, row, bar);
+        tma_rows(dst + kTailBytes / 2, &map_v, row, bar);
       }
       in = in + 1 == Sh::kDepth ? 0 : in + 1;
       ++issued;
       if (load.u + 1 == load.units) rows_end = 0;
       line.next(load);
     };
-    const int count = whi - wlo;
-    for (int d = 0; d < Sh::kDepth && d < count; ++d) issue();
     int out = 0, phase = 0;  // the stage of the next unit to use, and its barrier's parity
-
-    State<kTiles> s;
-    Query<kTiles> qr;
-    int pos = wlo;
-    for (int k = 0; k < count;) {
-      const Segment seg{pos - use.u, pos - use.u + use.units, use.b, use.seg};
-      const int piece = min(use.units - use.u, whi - pos);
-      const int head0 = use.seg / chunks * a.group + use.seg % chunks * Sh::kHeads;
-      const int live = min(Sh::kHeads, a.group - use.seg % chunks * Sh::kHeads);
-      const bool whole = piece == use.units;
-      qr.load(a, use.b, head0, live);
+    // One turn of the loop puts away the piece of the last turn while the queries of the next
+    // one are on their way.  What a warp runs once or twice is paid for in instruction fetches:
+    // it stands in one place where it can, and is not unrolled.
+    int pos = wlo, k = 0, piece = 0;
+    Segment seg{};
+#pragma unroll 1
+    for (;;) {
+      const bool more = k < count;
+      if (more) qr.fetch(a, use.b, line.head(use.h, use.ch), line.live(use.ch));
+      if (k > 0) {
+        // this lane's channels of head j: 32 q + 4 i .. + 3
+        const int i = lane >> 2, j = lane & 3;
+        const int head0 = line.head(seg.h, seg.ch), live = line.live(seg.ch);
+        const bool whole = piece == seg.end - seg.begin;
+        float* const part = pos == whi ? smem_part(warp) : global_part(warp);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            s.l[t] += __shfl_xor_sync(kFull, s.l[t], o);
+            s.z0[t] += __shfl_xor_sync(kFull, s.z0[t], o);
+            s.z1[t] += __shfl_xor_sync(kFull, s.z1[t], o);
+          }
+          const int g = 4 * t + j;
+          if (g >= live) continue;
+          float* to = whole ? a.o + (int64_t)seg.b * a.o_batch_stride + (int64_t)(head0 + g) * a.o_head_stride : part + g * kPart;
+          const float inv = whole ? inverse(s.l[t]) : 1.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float z = q < 2 ? s.z0[t] : s.z1[t];
+            float4 v;
+            v.x = (s.acc[2 * q][t][0] + s.acc[2 * q][t][1] + z) * inv;
+            v.y = (s.acc[2 * q][t][2] + s.acc[2 * q][t][3] + z) * inv;
+            v.z = (s.acc[2 * q + 1][t][0] + s.acc[2 * q + 1][t][1] + z) * inv;
+            v.w = (s.acc[2 * q + 1][t][2] + s.acc[2 * q + 1][t][3] + z) * inv;
+            *reinterpret_cast<float4*>(to + 32 * q + 4 * i) = v;
+          }
+          if (i == 0) {
+            if (!whole) *reinterpret_cast<float2*>(to + kD) = make_float2(s.m[t], s.l[t]);
+            else if (a.lse) a.lse[(size_t)seg.b * a.q_heads + head0 + g] = log_sum(s.m[t], s.l[t]);
+          }
+        }
+        if (pos - piece == wlo && lane == 0) s_first[warp] = part;
+        // the first piece of a segment in this CTA joins the others
+        if (!whole && pos - piece == max(seg.begin, clo)) {
+          if (lane == 0) s_own[warp][n_own] = seg;
+          ++n_own;
+        }
+      }
+      if (!more) break;
+      seg = Segment{pos - use.u, pos - use.u + use.units, use.b, use.h, use.ch};
+      piece = min(use.units - use.u, whi - pos);
       s.clear();
       const int tail_rows = use.n - FL_PAGE * paged_full(use.n);
+#pragma unroll 1
+      while (issued < count && issued < k + Sh::kDepth) issue();  // (the first turn)
+      qr.prepare();
+#pragma unroll 1
       for (int x = 0; x < piece; ++x, ++k) {
         if (!mbar_wait(&bars[warp][out], phase)) {
-          if (lane == 0) paged_error(a.x, FL_DEV_TIMEOUT, use.b);
+          if (lane == 0) errors.add(FL_DEV_TIMEOUT, use.b);
+#pragma unroll 1
           for (int d = 1; d < issued - k; ++d) {  // copies still in flight
             out = out + 1 == Sh::kDepth ? 0 : out + 1;
             if (out == 0) phase ^= 1;
@@ -706,7 +838,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         const unsigned st = smem_addr(st0) + out * kRec;
         const int tail = use.u + x - use.np;  // quarter of the tail, negative for a block
         if (tail >= 0) {
-          if (use.n > 0) tail_unit<kTiles>(st, min(kTailUnit, tail_rows - kTailUnit * tail), a, use.b, head0, live, s);
+          if (use.n > 0) tail_unit<kTiles>(st, min(kTailUnit, tail_rows - kTailUnit * tail), qr, s);
         } else if (!((voids >> out) & 1u)) {
           block_unit<kTiles>(st, qr, s);
         }
@@ -715,88 +847,61 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         __syncwarp();
         if (issued < count) issue();
       }
-      // this lane's channels of head j: 32 q + 4 i .. + 3
-      const int i = lane >> 2, j = lane & 3;
       pos += piece;
       use.u += piece - 1;
       line.next(use);
-      float* part = pos == whi ? smem_part(warp) : global_part(warp);
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          s.l[t] += __shfl_xor_sync(kFull, s.l[t], o);
-          s.z0[t] += __shfl_xor_sync(kFull, s.z0[t], o);
-          s.z1[t] += __shfl_xor_sync(kFull, s.z1[t], o);
-        }
-        const int g = 4 * t + j;
-        if (g >= live) continue;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float z = q < 2 ? s.z0[t] : s.z1[t];
-          float4 v;
-          v.x = s.acc[2 * q][t][0] + s.acc[2 * q][t][1] + z;
-          v.y = s.acc[2 * q][t][2] + s.acc[2 * q][t][3] + z;
-          v.z = s.acc[2 * q + 1][t][0] + s.acc[2 * q + 1][t][1] + z;
-          v.w = s.acc[2 * q + 1][t][2] + s.acc[2 * q + 1][t][3] + z;
-          if (whole) write_head(a, seg.b, head0 + g, 32 * q + 4 * i, v, s.m[t], s.l[t], q == 0 && i == 0);
-          else *reinterpret_cast<float4*>(part + g * kPart + 32 * q + 4 * i) = v;
-        }
-        if (!whole && i == 0) *reinterpret_cast<float2*>(part + g * kPart + kD) = make_float2(s.m[t], s.l[t]);
-      }
-      // the first piece of a segment in this CTA joins the others
-      if (!whole && pos - piece == max(seg.begin, clo)) {
-        own[n_own == 0 ? 0 : 1] = seg;
-        ++n_own;
-      }
     }
   }
+  if (lane == 0) s_owned[warp] = n_own;
+  errors.tell(a.x);
   __syncthreads();
 
-  for (int k = 0; k < n_own; ++k) {
-    const Segment seg = k == 0 ? own[0] : own[1];
-    // this warp and the next ones up to w1 hold its pieces
-    const int to = min(seg.end, chi);
-    int w1 = warp;
-    while (warp_begin(w1 + 1) < to) ++w1;
-    const bool first_moved = whi > seg.end;  // the segment ended inside this warp's part
-    const int c_head = seg.seg % chunks * Sh::kHeads;
-    const int head0 = seg.seg / chunks * a.group + c_head, live = min(Sh::kHeads, a.group - c_head);
-    const bool inside = seg.begin >= clo && seg.end <= chi;
-    const int c0 = (int)(((int64_t)(seg.begin + 1) * ctas - 1) / total), c1 = (int)(((int64_t)seg.end * ctas - 1) / total);
-    float* mine = cta_parts + (size_t)(2 * blockIdx.x + (seg.begin < clo ? 0 : 1)) * Sh::kHeads * kPart;
-    for (int g = 0; g < live; ++g) {
+  // head g of the segments that warp w holds is joined by warp w + g
+#pragma unroll 1
+  for (int g = 0; g < min(Sh::kHeads, a.group); ++g) {
+    const int w0 = warp >= g ? warp - g : warp - g + Sh::kWarps;
+#pragma unroll 1
+    for (int k = 0; k < s_owned[w0]; ++k) {
+      const Segment seg = s_own[w0][k];
+      if (g >= line.live(seg.ch)) continue;
+      // warp w0 and the next ones hold its pieces: w0's is its last one unless the segment ended
+      // inside its part, the others continue the segment with their first
+      const float* const piece0 = s_begin[w0 + 1] > seg.end ? global_part(w0) : smem_part(w0);
+      int n = 1, c0 = -1;
+      while (s_begin[w0 + n] < min(seg.end, chi)) ++n;
+      // several CTAs may share the segment (c0 .. c1): the last one to arrive joins their states
+      const bool inside = seg.begin >= clo && seg.end <= chi;
       float4 o;
       float m, l;
-      join<false>(w1 - warp + 1, [&](int x) -> const float* {
-        const int w = warp + x;
-        const bool last = x == 0 ? !first_moved : warp_begin(w + 1) <= seg.end;
-        return (last ? smem_part(w) : global_part(w)) + g * kPart;
-      }, o, m, l);
-      if (inside) {
-        write_head(a, seg.b, head0 + g, 4 * lane, o, m, l, lane == 0);
-      } else {
-        *(reinterpret_cast<float4*>(mine + g * kPart) + lane) = o;
-        if (lane == 0) *reinterpret_cast<float2*>(mine + g * kPart + kD) = make_float2(m, l);
+      auto cta_part = [&](int c) { return cta_parts + ((size_t)(2 * c + (c == c0 ? 1 : 0)) * Sh::kHeads + g) * kPart; };
+#pragma unroll 1
+      for (;;) {
+        join(n, [&](int x) -> const float* {
+          if (c0 >= 0) return cta_part(c0 + x);
+          return (x == 0 ? piece0 : s_first[w0 + x]) + g * kPart;
+        }, o, m, l);
+        if (inside || c0 >= 0) {
+          const int head = line.head(seg.h, seg.ch) + g;
+          const float inv = inverse(l);
+          *reinterpret_cast<float4*>(a.o + (int64_t)seg.b * a.o_batch_stride + (int64_t)head * a.o_head_stride + 4 * lane) =
+              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+          if (lane == 0 && a.lse) a.lse[(size_t)seg.b * a.q_heads + head] = log_sum(m, l);
+          break;
+        }
+        c0 = (int)(((int64_t)(seg.begin + 1) * ctas - 1) / total);
+        n = (int)(((int64_t)seg.end * ctas - 1) / total) - c0 + 1;
+        float* mine = cta_part(blockIdx.x);
+        *(reinterpret_cast<float4*>(mine) + lane) = o;
+        if (lane == 0) *reinterpret_cast<float2*>(mine + kD) = make_float2(m, l);
+        __threadfence();
+        __syncwarp();
+        int32_t* ticket = a.tickets + c0 * 8 + g;
+        int last = 0;
+        if (lane == 0) last = atomicAdd(ticket, 1) == n - 1;
+        if (!__shfl_sync(kFull, last, 0)) break;
+        __threadfence();
+        if (lane == 0) *ticket = 0;
       }
-    }
-    if (inside) continue;
-    // several CTAs share the segment: the last one to arrive joins their states
-    __threadfence();
-    __syncwarp();
-    int last = 0;
-    if (lane == 0) last = atomicAdd(&a.tickets[c0], 1) == c1 - c0;
-    last = __shfl_sync(kFull, last, 0);
-    if (!last) continue;
-    __threadfence();
-    if (lane == 0) a.tickets[c0] = 0;
-    for (int g = 0; g < live; ++g) {
-      float4 o;
-      float m, l;
-      join<true>(c1 - c0 + 1, [&](int x) -> const float* {
-        return cta_parts + ((size_t)(2 * (c0 + x) + (x == 0 ? 1 : 0)) * Sh::kHeads + g) * kPart;
-      }, o, m, l);
-      write_head(a, seg.b, head0 + g, 4 * lane, o, m, l, lane == 0);
     }
   }
 }

@@ -19,7 +19,7 @@ MAX_BATCH = 8192
 MAX_SLOTS = 131072
 MAX_BLOCKS = 16384
 MAX_KEEP = 16384
-WS_HEAD = 4096
+WS_HEAD = 8192
 
 # device error codes beside abi's (include/flashloop_paged.h)
 (FL_DEV_SLOT_RANGE, FL_DEV_SLOT_TWICE, FL_DEV_NO_PAGE, FL_DEV_TOO_LONG, FL_DEV_COUNT, FL_DEV_PAGE_RANGE,
