@@ -643,6 +643,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
   __shared__ Segment s_own[Sh::kWarps][2];  // segments whose first piece in this CTA a warp holds
   __shared__ int s_owned[Sh::kWarps];
   __shared__ int s_begin[Sh::kWarps + 1];       // the warps' stretches
+  __shared__ int s_total, s_ctas;
   __shared__ const float* s_first[Sh::kWarps];  // where the state of a warp's first piece is
   uint8_t* stages = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -682,6 +683,10 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     errors.tell(a.x);
     return;
   }
+  if (threadIdx.x == 0) {
+    s_total = total;
+    s_ctas = ctas;
+  }
   const int clo = (int)((int64_t)total * blockIdx.x / ctas), chi = (int)((int64_t)total * (blockIdx.x + 1) / ctas);
   // (with fewer units than warps the last warps have none)
   if (threadIdx.x <= Sh::kWarps)
@@ -704,11 +709,10 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
   fence_proxy_async();
 
   // states of pieces: the last one of a warp in its own stages, one before it in the workspace
-  float* parts = static_cast<float*>(a.data);
-  float* warp_parts = parts + (size_t)(blockIdx.x * Sh::kWarps) * Sh::kHeads * kPart;
-  float* cta_parts = parts + (size_t)kMaxCtas * Sh::kWarps * Sh::kHeads * kPart;
   auto smem_part = [&](int w) { return reinterpret_cast<float*>(stages + (size_t)w * Sh::kDepth * kRec); };
-  auto global_part = [&](int w) { return warp_parts + (size_t)w * Sh::kHeads * kPart; };
+  auto global_part = [&](int w) {
+    return static_cast<float*>(a.data) + (size_t)(blockIdx.x * Sh::kWarps + w) * Sh::kHeads * kPart;
+  };
 
   int n_own = 0;
   if (wlo < whi) {
@@ -809,7 +813,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         }
         if (pos - piece == wlo && lane == 0) s_first[warp] = part;
         // the first piece of a segment in this CTA joins the others
-        if (!whole && pos - piece == max(seg.begin, clo)) {
+        if (!whole && pos - piece == max(seg.begin, s_begin[0])) {
           if (lane == 0) s_own[warp][n_own] = seg;
           ++n_own;
         }
@@ -856,7 +860,9 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
   errors.tell(a.x);
   __syncthreads();
 
-  // head g of the segments that warp w holds is joined by warp w + g
+  // head g of the segments that warp w holds is joined by warp w + g.  (The stretches are read
+  // again: kept in registers over the loop above they would be spilled.)
+  const int first = s_begin[0], last = s_begin[Sh::kWarps];
 #pragma unroll 1
   for (int g = 0; g < min(Sh::kHeads, a.group); ++g) {
     const int w0 = warp >= g ? warp - g : warp - g + Sh::kWarps;
@@ -868,12 +874,14 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       // inside its part, the others continue the segment with their first
       const float* const piece0 = s_begin[w0 + 1] > seg.end ? global_part(w0) : smem_part(w0);
       int n = 1, c0 = -1;
-      while (s_begin[w0 + n] < min(seg.end, chi)) ++n;
+      while (s_begin[w0 + n] < min(seg.end, last)) ++n;
       // several CTAs may share the segment (c0 .. c1): the last one to arrive joins their states
-      const bool inside = seg.begin >= clo && seg.end <= chi;
+      const bool inside = seg.begin >= first && seg.end <= last;
       float4 o;
       float m, l;
-      auto cta_part = [&](int c) { return cta_parts + ((size_t)(2 * c + (c == c0 ? 1 : 0)) * Sh::kHeads + g) * kPart; };
+      auto cta_part = [&](int c) {
+        return static_cast<float*>(a.data) + (((size_t)kMaxCtas * Sh::kWarps + 2 * c + (c == c0 ? 1 : 0)) * Sh::kHeads + g) * kPart;
+      };
 #pragma unroll 1
       for (;;) {
         join(n, [&](int x) -> const float* {
@@ -888,17 +896,17 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
           if (lane == 0 && a.lse) a.lse[(size_t)seg.b * a.q_heads + head] = log_sum(m, l);
           break;
         }
-        c0 = (int)(((int64_t)(seg.begin + 1) * ctas - 1) / total);
-        n = (int)(((int64_t)seg.end * ctas - 1) / total) - c0 + 1;
+        c0 = (int)(((uint64_t)(seg.begin + 1) * s_ctas - 1) / (unsigned)s_total);
+        n = (int)(((uint64_t)seg.end * s_ctas - 1) / (unsigned)s_total) - c0 + 1;
         float* mine = cta_part(blockIdx.x);
         *(reinterpret_cast<float4*>(mine) + lane) = o;
         if (lane == 0) *reinterpret_cast<float2*>(mine + kD) = make_float2(m, l);
         __threadfence();
         __syncwarp();
         int32_t* ticket = a.tickets + c0 * 8 + g;
-        int last = 0;
-        if (lane == 0) last = atomicAdd(ticket, 1) == n - 1;
-        if (!__shfl_sync(kFull, last, 0)) break;
+        int done = 0;
+        if (lane == 0) done = atomicAdd(ticket, 1) == n - 1;
+        if (!__shfl_sync(kFull, done, 0)) break;
         __threadfence();
         if (lane == 0) *ticket = 0;
       }
