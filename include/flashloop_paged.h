@@ -142,7 +142,7 @@ fl_status fl_paged_workspace_init(void* ws, size_t ws_bytes, void* stream);
  * With lo_c = z_c and hi_c = z_c + 15 s_c from the record's key groups
  *     score(block) = max over the group's queries q of sum_c max(q_c lo_c, q_c hi_c),
  * the largest score any key of the block could have; summed in fp64, ties to the lower
- * block, NaN below every number.  q as in fl_paged_attn_decode. */
+ * block; blocks whose scales or zeros are not finite, or whose score is NaN, come last.  q as in fl_paged_attn_decode. */
 fl_status fl_paged_select(const fl_paged_index* index, const fl_paged_pool* pool, int32_t batch, const int32_t* slots,
                           int32_t q_heads, const uint16_t* q, int64_t q_batch_stride, int64_t q_head_stride,
                           int32_t keep, int32_t* sel, void* ws, size_t ws_bytes, void* stream);
