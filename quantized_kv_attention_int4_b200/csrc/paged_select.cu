@@ -36,7 +36,8 @@ template <int kG>
 __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
   extern __shared__ int32_t prefix[];
   __shared__ int red[kST / 32];
-  __shared__ alignas(16) double s_q[kG][kD];  // times 2^500
+  // high words of 2^500 q and of 2^500 15 max(q, 0): 8 and 12 significant bits, their low words are 0
+  __shared__ alignas(16) int s_q[2][kG][kD];
   grid_dep_launch();
   const int tid = threadIdx.x, heads = a.p.kv_heads;
   const fl_paged_index& x = a.x;
@@ -72,7 +73,13 @@ __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
       best[r] = -INFINITY;
-      nan[r] = rec[r] == nullptr;  // a block that cannot be read ranks last
+      // infinite or NaN scales and zeros (exponent 31) carry into the halves' top bits
+      uint32_t over = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) over |= ((&sz[r][e].x)[c] & 0x7fff7fffu) + 0x04000400u;
+      nan[r] = rec[r] == nullptr || (over & 0x80008000u);  // such a block, or one that cannot be read, ranks last
     }
     for (int g0 = 0; g0 < a.group; g0 += kG) {
       __syncthreads();
@@ -80,45 +87,51 @@ __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
       for (int i = tid; i < kG * kD; i += kST) {
         const int g = min(g0 + i / kD, a.group - 1);
         const uint16_t q = a.q[(int64_t)b * a.q_batch_stride + (int64_t)(h * a.group + g) * a.q_head_stride + i % kD];
-        s_q[i / kD][i % kD] = (double)__uint_as_float((uint32_t)q << 16) * 0x1p500;
+        const double v = (double)__uint_as_float((uint32_t)q << 16) * 0x1p500;
+        s_q[0][i / kD][i % kD] = __double2hiint(v);
+        s_q[1][i / kD][i % kD] = __double2hiint(v > 0.0 ? 15.0 * v : 0.0);
       }
       __syncthreads();
+      double sum[kRounds][kG];
 #pragma unroll
-      for (int r = 0; r < kRounds; ++r) {
-        double sum[kG];
+      for (int r = 0; r < kRounds; ++r)
 #pragma unroll
-        for (int g = 0; g < kG; ++g) sum[g] = 0.0;
+        for (int g = 0; g < kG; ++g) sum[r][g] = 0.0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          double lo[4], hi[4];
+      for (int e = 0; e < 4; ++e) {
+        // sum_c max(q lo, q hi) = sum_c q lo + 15 max(q, 0) s
+        double lo[kRounds][4], sc[kRounds][4];
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint32_t v = (&sz[r][e].x)[c];
-            const double scale = __hiloint2double((int)((v & 0x7fffu) << 10), 0);
-            lo[c] = __hiloint2double((int)(((v >> 6) & 0x01fffc00u) | (v & 0x80000000u)), 0);
-            hi[c] = fma(15.0, scale, lo[c]);
-            // infinite or NaN scales and zeros (exponent 31)
-            nan[r] |= (v & 0x7c00u) == 0x7c00u || (v & 0x7c000000u) == 0x7c000000u;
+            uint32_t v = (&sz[r][e].x)[c];
+            asm volatile("" : "+r"(v));  // widened here each time: 128 registers if hoisted out of the loop
+            sc[r][c] = __hiloint2double((int)((v & 0x7fffu) << 10), 0);
+            lo[r][c] = __hiloint2double((int)(((v >> 6) & 0x01fffc00u) | (v & 0x80000000u)), 0);
           }
 #pragma unroll
-          for (int g = 0; g < kG; ++g) {
-            const double2 qa = *reinterpret_cast<const double2*>(&s_q[g][32 * e + 4 * sub]);
-            const double2 qb = *reinterpret_cast<const double2*>(&s_q[g][32 * e + 4 * sub + 2]);
-            sum[g] = fma(qa.x, __double2hiint(qa.x) > 0 ? hi[0] : lo[0], sum[g]);
-            sum[g] = fma(qa.y, __double2hiint(qa.y) > 0 ? hi[1] : lo[1], sum[g]);
-            sum[g] = fma(qb.x, __double2hiint(qb.x) > 0 ? hi[2] : lo[2], sum[g]);
-            sum[g] = fma(qb.y, __double2hiint(qb.y) > 0 ? hi[3] : lo[3], sum[g]);
+        for (int g = 0; g < kG; ++g) {
+          const int4 qa = *reinterpret_cast<const int4*>(&s_q[0][g][32 * e + 4 * sub]);
+          const int4 qb = *reinterpret_cast<const int4*>(&s_q[1][g][32 * e + 4 * sub]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const double q = __hiloint2double((&qa.x)[c], 0), p = __hiloint2double((&qb.x)[c], 0);
+#pragma unroll
+            for (int r = 0; r < kRounds; ++r) sum[r][g] = fma(p, sc[r][c], fma(q, lo[r][c], sum[r][g]));
           }
         }
+      }
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r)
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
 #pragma unroll
-          for (int o = 1; o < 8; o <<= 1) sum[g] += __shfl_xor_sync(kFull, sum[g], o);
-          sum[g] *= 0x1p508;
-          nan[r] |= sum[g] != sum[g];
-          best[r] = fmax(best[r], sum[g]);
+          for (int o = 1; o < 8; o <<= 1) sum[r][g] += __shfl_xor_sync(kFull, sum[r][g], o);
+          sum[r][g] *= 0x1p508;
+          nan[r] |= sum[r][g] != sum[r][g];
+          best[r] = fmax(best[r], sum[r][g]);
         }
-      }
     }
     unsigned long long* out = static_cast<unsigned long long*>(a.data) + ((size_t)b * heads + h) * x.max_pages;
 #pragma unroll
