@@ -3,9 +3,10 @@
 // score(block) = max over the group's queries of sum_c max(q_c lo_c, q_c hi_c), with lo = z
 // and hi = z + 15 s of the record's key groups: the largest q.k any key of the block could
 // have, from 512 of the record's 9216 bytes.  Two launches, the second one's start overlapped:
-//   score_kernel  eight lanes a block, 16 channels each; every product is exact in fp64 (8
-//                 significant bits times at most 45), so scores of equal blocks are equal
-//                 and the order is the definition's but for differences of a few 1e-16.
+//   score_kernel  sum_c max(q lo, q hi) = sum_c q lo + 15 max(q, 0) s as two fp64 matrix
+//                 products, 8 blocks x 8 queries at a time.  Every product is exact (8 or 12
+//                 significant bits times 11), so scores of equal blocks are equal and the
+//                 order is the definition's but for differences of a few 1e-16.
 //                 A binary16 number becomes an fp64 one by moving its bits (no conversion
 //                 instruction, which the SM issues at a quarter of this rate): the exponent
 //                 keeps its bias, which scales the number by 2^-1008, subnormals included;
@@ -18,9 +19,8 @@
 namespace fl {
 namespace {
 
-constexpr int kST = 256;   // threads of the score kernel: 32 blocks a round
-constexpr int kRounds = 2;
-constexpr int kChunk = 32 * kRounds;
+constexpr int kST = 256;   // threads of the score kernel: 8 blocks a warp
+constexpr int kChunk = 64; // blocks it takes at a time
 constexpr int kTT = 256;   // threads of the top-k kernel
 constexpr int kHeld = 8;   // keys a thread of it holds
 constexpr int kDigit = 10;
@@ -31,115 +31,145 @@ __device__ __forceinline__ unsigned long long score_image(double v) {
   return (unsigned long long)(b < 0 ? ~b : b | (long long)0x8000000000000000ull);
 }
 
-// kG queries of a group at a time (a group's last ones are repeated to fill them).
-template <int kG>
+// c += a b for 8 x 4 by 4 x 8: lane (i, j) holds a[i][j], b[j][i], c[i][2 j], c[i][2 j + 1].
+__device__ __forceinline__ void mma_f64(double (&c)[2], double a, double b) {
+  asm("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};" : "+d"(c[0]), "+d"(c[1]) : "d"(a), "d"(b));
+}
+
+// Eight queries of a group at a time (its last one is repeated to fill them).  A CTA takes an
+// equal, consecutive share of the chunks of 64 blocks, so that it stages the queries of an
+// (entry, head) once; while it computes on a chunk, the records of the next one and the page
+// numbers of the one after are on their way.  Lane (i, j) reads channels 16 m + 4 j + t of
+// block i, and these are the columns of product (m, t).
 __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
   extern __shared__ int32_t prefix[];
   __shared__ int red[kST / 32];
-  // high words of 2^500 q and of 2^500 15 max(q, 0): 8 and 12 significant bits, their low words are 0
-  __shared__ alignas(16) int s_q[2][kG][kD];
+  // per product pair (m, t / 2) and lane: 2^500 q, and 2^500 15 max(q, 0), of channels t, t + 1
+  __shared__ double2 s_q[2][16][32];
   grid_dep_launch();
-  const int tid = threadIdx.x, heads = a.p.kv_heads;
+  const int tid = threadIdx.x, lane = tid & 31, i = lane >> 2, j = lane & 3, heads = a.p.kv_heads;
   const fl_paged_index& x = a.x;
   const bool tell = blockIdx.x == 0;
   const int total = paged_scan<kST>(a.batch, prefix, red, [&](int b) {
     const int s = paged_slot(x, a.slots, b, tell);
     if (s < 0) return 0;
     const int full = paged_full(paged_length(x, s, b, tell));
-    return full > a.keep ? (full + kChunk - 1) / kChunk : 0;
+    return full > a.keep ? (full + kChunk - 1) / kChunk * heads : 0;
   });
-  const int sub = tid & 7, blk = tid >> 3;
-  for (int64_t w = blockIdx.x; w < (int64_t)total * heads; w += gridDim.x) {
-    const int item = (int)(w / heads), h = (int)(w % heads);
-    const int b = paged_find(prefix, a.batch, item), c0 = (item - prefix[b]) * kChunk;
-    const int s = paged_slot(x, a.slots, b, false);
-    const int full = paged_full(paged_length(x, s, b, false));
-    const uint8_t* rec[kRounds];
+  int w = (int)((int64_t)total * blockIdx.x / gridDim.x);
+  const int end = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+  if (w >= end) return;
+
+  struct At {
+    int b, h, c, chunks, slot, full;  // entry, head, chunk of its blocks
+  };
+  auto enter = [&](At& p, int b) {
+    p.b = b;
+    p.slot = paged_slot(x, a.slots, b, false);
+    p.full = paged_full(paged_length(x, p.slot, b, false));
+    p.chunks = (p.full + kChunk - 1) / kChunk;
+  };
+  auto next = [&](At& p) {
+    if (++p.c < p.chunks) return;
+    p.c = 0;
+    if (++p.h < heads) return;
+    p.h = 0;
+    int b = p.b + 1;
+    while (b < a.batch && prefix[b + 1] == prefix[b]) ++b;
+    if (b < a.batch) enter(p, b);
+  };
+  auto page_of = [&](const At& p) {
+    const int block = p.c * kChunk + (tid >> 2);
+    if (block >= p.full) return -1;
+    const int page = __ldg(x.table + (int64_t)p.slot * x.max_pages + block);
+    if (page >= 0 && page < x.pages) return page;
+    if (j == 0) paged_error(x, FL_DEV_PAGE_RANGE, p.b);
+    return -1;
+  };
+  auto scales = [&](const At& p, int page, uint4 (&sz)[8]) {
+    const uint8_t* rec = a.p.rec + ((size_t)max(page, 0) * heads + p.h) * kRec + kRecKsz + 16 * j;
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      const int block = c0 + 32 * r + blk;
-      const int page = block < full ? __ldg(x.table + (int64_t)s * x.max_pages + block) : -1;
-      const bool ok = page >= 0 && page < x.pages;
-      if (block < full && !ok && sub == 0) paged_error(x, FL_DEV_PAGE_RANGE, b);
-      rec[r] = ok ? a.p.rec + ((size_t)page * heads + h) * kRec + kRecKsz : nullptr;
+    for (int m = 0; m < 8; ++m) sz[m] = ldg_u4(rec + 64 * m);
+  };
+  At cur, ahead;
+  enter(cur, paged_find(prefix, a.batch, w));
+  cur.h = (w - prefix[cur.b]) / cur.chunks;
+  cur.c = (w - prefix[cur.b]) % cur.chunks;
+  ahead = cur;
+  int page = page_of(cur), page1 = -1;
+  if (w + 1 < end) {
+    next(ahead);  // ahead is the chunk behind the current one
+    page1 = page_of(ahead);
+  }
+  uint4 sz[8], sz1[8];
+  scales(cur, page, sz);
+  int staged_b = -1, staged_h = -1;
+  for (; w < end; ++w) {
+    At after = ahead;
+    int page2 = -1;
+    if (w + 1 < end) scales(ahead, page1, sz1);
+    if (w + 2 < end) {
+      next(after);
+      page2 = page_of(after);
     }
-    uint4 sz[kRounds][4];
+    // infinite or NaN scales and zeros (exponent 31) carry into the halves' top bits; such a
+    // block, or one that cannot be read, ranks last
+    uint32_t over = 0;
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r)
+    for (int m = 0; m < 8; ++m)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sz[r][e] = rec[r] ? ldg_u4(rec[r] + 128 * e + 16 * sub) : make_uint4(0u, 0u, 0u, 0u);
-    double best[kRounds];
-    bool nan[kRounds];
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      best[r] = -INFINITY;
-      // infinite or NaN scales and zeros (exponent 31) carry into the halves' top bits
-      uint32_t over = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) over |= ((&sz[r][e].x)[c] & 0x7fff7fffu) + 0x04000400u;
-      nan[r] = rec[r] == nullptr || (over & 0x80008000u);  // such a block, or one that cannot be read, ranks last
-    }
-    for (int g0 = 0; g0 < a.group; g0 += kG) {
-      __syncthreads();
-#pragma unroll
-      for (int i = tid; i < kG * kD; i += kST) {
-        const int g = min(g0 + i / kD, a.group - 1);
-        const uint16_t q = a.q[(int64_t)b * a.q_batch_stride + (int64_t)(h * a.group + g) * a.q_head_stride + i % kD];
-        const double v = (double)__uint_as_float((uint32_t)q << 16) * 0x1p500;
-        s_q[0][i / kD][i % kD] = __double2hiint(v);
-        s_q[1][i / kD][i % kD] = __double2hiint(v > 0.0 ? 15.0 * v : 0.0);
+      for (int c = 0; c < 4; ++c) over |= ((&sz[m].x)[c] & 0x7fff7fffu) + 0x04000400u;
+    bool nan = page < 0 || (over & 0x80008000u);
+    double best = -INFINITY;
+    for (int g0 = 0; g0 < a.group; g0 += 8) {
+      if (a.group > 8 || cur.b != staged_b || cur.h != staged_h) {
+        __syncthreads();
+        for (int y = tid; y < 1024; y += kST) {  // query y / 128, channel y % 128
+          const int g = min(g0 + (y >> 7), a.group - 1), ch = y & 127;
+          const uint16_t q = a.q[(int64_t)cur.b * a.q_batch_stride + (int64_t)(cur.h * a.group + g) * a.q_head_stride + ch];
+          const double v = (double)__uint_as_float((uint32_t)q << 16) * 0x1p500;
+          double* to = &s_q[0][ch >> 4 << 1 | (ch >> 1 & 1)][(y >> 7) << 2 | (ch >> 2 & 3)].x + (ch & 1);
+          to[0] = v;
+          to[2 * 16 * 32] = v > 0.0 ? 15.0 * v : 0.0;
+        }
+        staged_b = cur.b;
+        staged_h = cur.h;
+        __syncthreads();
       }
-      __syncthreads();
-      double sum[kRounds][kG];
+      double sum[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
 #pragma unroll
-      for (int r = 0; r < kRounds; ++r)
+      for (int m = 0; m < 8; ++m)
 #pragma unroll
-        for (int g = 0; g < kG; ++g) sum[r][g] = 0.0;
+        for (int t = 0; t < 4; t += 2) {
+          const double2 q = s_q[0][2 * m + t / 2][lane], p = s_q[1][2 * m + t / 2][lane];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // sum_c max(q lo, q hi) = sum_c q lo + 15 max(q, 0) s
-        double lo[kRounds][4], sc[kRounds][4];
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v = (&sz[r][e].x)[c];
-            asm volatile("" : "+r"(v));  // widened here each time: 128 registers if hoisted out of the loop
-            sc[r][c] = __hiloint2double((int)((v & 0x7fffu) << 10), 0);
-            lo[r][c] = __hiloint2double((int)(((v >> 6) & 0x01fffc00u) | (v & 0x80000000u)), 0);
-          }
-#pragma unroll
-        for (int g = 0; g < kG; ++g) {
-          const int4 qa = *reinterpret_cast<const int4*>(&s_q[0][g][32 * e + 4 * sub]);
-          const int4 qb = *reinterpret_cast<const int4*>(&s_q[1][g][32 * e + 4 * sub]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const double q = __hiloint2double((&qa.x)[c], 0), p = __hiloint2double((&qb.x)[c], 0);
-#pragma unroll
-            for (int r = 0; r < kRounds; ++r) sum[r][g] = fma(p, sc[r][c], fma(q, lo[r][c], sum[r][g]));
+          for (int y = 0; y < 2; ++y) {
+            uint32_t v = (&sz[m].x)[t + y];
+            asm volatile("" : "+r"(v));  // widened here each time: 128 registers more if hoisted out of the loop
+            mma_f64(sum[0], __hiloint2double((int)(((v >> 6) & 0x01fffc00u) | (v & 0x80000000u)), 0), y ? q.y : q.x);
+            mma_f64(sum[1], __hiloint2double((int)((v & 0x7fffu) << 10), 0), y ? p.y : p.x);
           }
         }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const double v = (sum[0][y] + sum[1][y]) * 0x1p508;
+        nan |= v != v;
+        best = fmax(best, v);
       }
-#pragma unroll
-      for (int r = 0; r < kRounds; ++r)
-#pragma unroll
-        for (int g = 0; g < kG; ++g) {
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) sum[r][g] += __shfl_xor_sync(kFull, sum[r][g], o);
-          sum[r][g] *= 0x1p508;
-          nan[r] |= sum[r][g] != sum[r][g];
-          best[r] = fmax(best[r], sum[r][g]);
-        }
     }
-    unsigned long long* out = static_cast<unsigned long long*>(a.data) + ((size_t)b * heads + h) * x.max_pages;
+    // the block's best over the four lanes of its queries
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      const int block = c0 + 32 * r + blk;
-      const bool bad = __reduce_or_sync(kFull, nan[r] ? 1u << (threadIdx.x >> 3 & 3) : 0u) >> (threadIdx.x >> 3 & 3) & 1u;
-      if (sub == 0 && block < full) out[block] = bad ? 0ull : score_image(best[r]);
-    }
+    for (int o = 1; o < 4; o <<= 1) best = fmax(best, __shfl_xor_sync(kFull, best, o));
+    const bool bad = (__ballot_sync(kFull, nan) >> (4 * i)) & 15u;
+    const int block = cur.c * kChunk + (tid >> 2);
+    if (j == 0 && block < cur.full)
+      (static_cast<unsigned long long*>(a.data) + ((size_t)cur.b * heads + cur.h) * x.max_pages)[block] = bad ? 0ull : score_image(best);
+    cur = ahead;
+    ahead = after;
+    page = page1;
+    page1 = page2;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) sz[m] = sz1[m];
   }
 }
 
@@ -284,14 +314,6 @@ __global__ void __launch_bounds__(kTT) topk_kernel(PagedAttnArgs a) {
   else topk<false>(key, n, k, sel);
 }
 
-template <int kG>
-cudaError_t launch_score(const PagedAttnArgs& a, int sms, cudaStream_t s) {
-  const int64_t items = (int64_t)a.batch * ((a.x.max_pages + kChunk - 1) / kChunk) * a.p.kv_heads;
-  const int grid = (int)(items < 4 * sms ? items : 4 * sms);
-  score_kernel<kG><<<grid, kST, (size_t)(a.batch + 1) * 4, s>>>(a);
-  return cudaGetLastError();
-}
-
 }  // namespace
 
 uint64_t paged_select_bytes(const fl_paged_index& x, const fl_paged_pool& p, int batch) {
@@ -304,10 +326,10 @@ cudaError_t launch_paged_select(const PagedAttnArgs& a, cudaStream_t s) {
   if (sms <= 0) return cudaErrorInvalidDevice;
   const bool scored = a.keep < a.x.max_pages;  // otherwise every request keeps all it has
   if (scored) {
-    const cudaError_t e = a.group == 1   ? launch_score<1>(a, sms, s)
-                          : a.group == 2 ? launch_score<2>(a, sms, s)
-                          : a.group <= 4 ? launch_score<4>(a, sms, s)
-                                         : launch_score<8>(a, sms, s);
+    const int64_t items = (int64_t)a.batch * ((a.x.max_pages + kChunk - 1) / kChunk) * a.p.kv_heads;
+    const int grid = (int)(items < 2 * sms ? items : 2 * sms);
+    score_kernel<<<grid, kST, (size_t)(a.batch + 1) * 4, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   return launch_pdl_if(scored, topk_kernel, dim3(a.p.kv_heads, a.batch), dim3(kTT), 0, s, a);
