@@ -42,6 +42,10 @@ namespace fl {
 namespace {
 
 constexpr int kMaxCtas = 160;
+// Units a CTA should have.  With 1 x 32768, 16 heads, 52 blocks kept (the whole step): 4, 6, 8
+// 23.0 us, 12 24.3, 24 28.3.
+constexpr int kMinUnits = 8;
+constexpr int kWarpScan = 128;     // entries up to which every warp scans the lengths by itself
 constexpr int kPart = 132;         // floats of a head's state: o[128], max, sum, -, -
 constexpr int kTailUnit = 16;      // tail rows of a unit
 constexpr int kTailBytes = 2 * kTailUnit * kD * 2;
@@ -635,7 +639,7 @@ __device__ __forceinline__ void join(int n, F&& part, float4& o, float& m, float
 template <int kTiles, bool kSel>
 __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     paged_attn_kernel(const PagedAttnArgs a, const __grid_constant__ CUtensorMap map_rec,
-                      const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, int min_units) {
+                      const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   using Sh = Shape<kTiles>;
   extern __shared__ uint8_t raw[];
   __shared__ alignas(8) uint64_t bars[Sh::kWarps][Sh::kDepth];
@@ -661,52 +665,108 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     }
   }
   // the line of units, then this CTA's and this warp's stretch of it
-  int32_t* prefix = reinterpret_cast<int32_t*>(stages);  // [batch + 1]
-  int32_t* lengths = prefix + a.batch + 1;                // [batch]
-  const int total = paged_scan<Sh::kThreads>(a.batch, prefix, red, [&](int b) {
+  auto length_of = [&](int b, bool tell) {  // -1: padded
     const int s = a.slots ? __ldg(a.slots + b) : b;
     if (s < 0 || s >= a.x.slots) {
-      if (s != -1 && blockIdx.x == 0) errors.add(FL_DEV_SLOT_RANGE, b);
-      return 0;
+      if (s != -1 && tell) errors.add(FL_DEV_SLOT_RANGE, b);
+      return -1;
     }
-    int n = a.x.length[s];
-    if (n < 0 || n > a.x.max_pages * FL_PAGE) {
-      if (blockIdx.x == 0) errors.add(FL_DEV_TOO_LONG, b);
-      n = 0;
+    const int n = a.x.length[s];
+    if (n >= 0 && n <= a.x.max_pages * FL_PAGE) return n;
+    if (tell) errors.add(FL_DEV_TOO_LONG, b);
+    return 0;
+  };
+  const int per_entry = heads * chunks;  // segments of an entry
+  int total = 0, most = 0, segments = 0;  // units, units of the longest segment
+  int clo, chi, wlo, whi;
+  // A small call takes fewer CTAs (a warp should have a unit).  One whose segments have all the
+  // same length takes one CTA each where that costs a warp a unit more at most: none is cut
+  // then, which saves the join between CTAs (1 x 256, 16 heads: 12.8 -> 8.5 us; 16 x 32768
+  // with 52 blocks kept, 8 x 4 heads, the whole step: 62.6 -> 57 us).
+  auto stretch = [&]() {
+    int ctas = min((int)gridDim.x, max(total / kMinUnits, 1));
+    if (segments > 0 && segments <= (int)gridDim.x && total == segments * most &&
+        most <= total / (int)gridDim.x + Sh::kWarps)
+      ctas = segments;
+    clo = (int)((int64_t)total * blockIdx.x / ctas);
+    chi = (int)blockIdx.x < ctas ? (int)((int64_t)total * (blockIdx.x + 1) / ctas) : clo;
+    // (with fewer units than warps the last warps have none)
+    const int n = chi - clo, q = n / Sh::kWarps, r = n % Sh::kWarps;
+    auto begin = [&](int w) { return n >= Sh::kWarps ? clo + q * w + r * w / Sh::kWarps : min(clo + w, chi); };
+    wlo = begin(warp);
+    whi = begin(warp + 1);
+    if (lane == 0) s_begin[warp] = wlo;
+    if (lane == 0 && warp == Sh::kWarps - 1) {
+      s_begin[Sh::kWarps] = whi;
+      s_total = total;
+      s_ctas = ctas;
     }
-    lengths[b] = n;
-    return line.units_of(n) * heads * chunks;
-  });
-  // a small call takes fewer CTAs: a warp should have a unit, and joins have their price
-  const int ctas = min((int)gridDim.x, max(total / min_units, 1));
-  if ((int)blockIdx.x >= ctas || total == 0) {
+  };
+  Cursor use{};
+  int left = 0;  // units of the entry before this warp's first one
+  if (a.batch <= kWarpScan) {
+    // every warp goes through the lengths by itself: entry 32 y + l in lane l
+    int n4[kWarpScan / 32], u4[kWarpScan / 32], p4[kWarpScan / 32];
+#pragma unroll
+    for (int y = 0; y < kWarpScan / 32; ++y) n4[y] = 32 * y + lane < a.batch ? length_of(32 * y + lane, blockIdx.x == 0 && warp == 0) : -1;
+#pragma unroll
+    for (int y = 0; y < kWarpScan / 32; ++y) {
+      u4[y] = p4[y] = 0;
+      if (32 * y >= a.batch) continue;
+      const int u = n4[y] < 0 ? 0 : line.units_of(n4[y]);
+      most = max(most, __reduce_max_sync(kFull, u));
+      segments += per_entry * __popc(__ballot_sync(kFull, u > 0));
+      u4[y] = u * per_entry;
+      int sum = u4[y];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFull, sum, o);
+        if (lane >= o) sum += v;
+      }
+      p4[y] = total + sum - u4[y];
+      total += __shfl_sync(kFull, sum, 31);
+    }
+    stretch();
+#pragma unroll
+    for (int y = 0; y < kWarpScan / 32; ++y) {
+      if (32 * y >= a.batch) continue;
+      const unsigned in = __ballot_sync(kFull, wlo < whi && p4[y] <= wlo && wlo < p4[y] + u4[y]);
+      if (in) {
+        const int l = __ffs(in) - 1;
+        use.b = 32 * y + l;
+        use.n = __shfl_sync(kFull, n4[y], l);
+        left = wlo - __shfl_sync(kFull, p4[y], l);
+      }
+    }
+  } else {
+    int32_t* prefix = reinterpret_cast<int32_t*>(stages);  // [batch + 1]
+    int32_t* lengths = prefix + a.batch + 1;                // [batch]
+    total = paged_scan<Sh::kThreads>(a.batch, prefix, red, [&](int b) {
+      const int n = length_of(b, blockIdx.x == 0);
+      lengths[b] = n;
+      return n < 0 ? 0 : line.units_of(n) * per_entry;
+    });
+    stretch();
+    if (wlo < whi) {
+      use.b = paged_find(prefix, a.batch, wlo);
+      use.n = lengths[use.b];
+      left = wlo - prefix[use.b];
+    }
+    __syncthreads();  // the stages take over from the prefix sums
+    fence_proxy_async();
+  }
+  if (clo == chi) {
     errors.tell(a.x);
     return;
   }
-  if (threadIdx.x == 0) {
-    s_total = total;
-    s_ctas = ctas;
-  }
-  const int clo = (int)((int64_t)total * blockIdx.x / ctas), chi = (int)((int64_t)total * (blockIdx.x + 1) / ctas);
-  // (with fewer units than warps the last warps have none)
-  if (threadIdx.x <= Sh::kWarps)
-    s_begin[threadIdx.x] = chi - clo >= Sh::kWarps ? clo + (int)((unsigned)((chi - clo) / Sh::kWarps) * threadIdx.x +
-                                                                 (unsigned)((chi - clo) % Sh::kWarps) * threadIdx.x / Sh::kWarps)
-                                                   : min(clo + (int)threadIdx.x, chi);
-  __syncthreads();
-  const int wlo = s_begin[warp], whi = s_begin[warp + 1];
-  Cursor use{};
   if (wlo < whi) {
-    use.b = paged_find(prefix, a.batch, wlo);
     use.slot = a.slots ? __ldg(a.slots + use.b) : use.b;
-    line.place(use, lengths[use.b]);
-    const int left = wlo - prefix[use.b], seg = left / use.units;
+    line.place(use, use.n);
+    const int seg = left / use.units;
     use.u = left - seg * use.units;
     use.h = chunks == 1 ? seg : seg / chunks;
     use.ch = seg - use.h * chunks;
   }
-  __syncthreads();  // the stages take over from the prefix sums
-  fence_proxy_async();
 
   // states of pieces: the last one of a warp in its own stages, one before it in the workspace
   auto smem_part = [&](int w) { return reinterpret_cast<float*>(stages + (size_t)w * Sh::kDepth * kRec); };
@@ -950,7 +1010,7 @@ cudaError_t launch(const PagedAttnArgs& a, int ctas, cudaStream_t s) {
   if (!rows_map(&rec, a.p.rec, (uint64_t)a.x.pages * a.p.kv_heads * (kRec / 128), kRec / 128) ||
       !rows_map(&tk, a.p.tail_k, tail_rows, 2 * kTailUnit) || !rows_map(&tv, a.p.tail_v, tail_rows, 2 * kTailUnit))
     return cudaErrorInvalidValue;
-  paged_attn_kernel<kTiles, kSel><<<ctas, Sh::kThreads, Sh::kSmem, s>>>(a, rec, tk, tv, Sh::kWarps);
+  paged_attn_kernel<kTiles, kSel><<<ctas, Sh::kThreads, Sh::kSmem, s>>>(a, rec, tk, tv);
   return cudaGetLastError();
 }
 

@@ -54,54 +54,58 @@ _c_select = abi._sig("fl_paged_select", _I, _XP, _PP, _I, _P, _I, _P, _L, _L, _I
 _c_attn = abi._sig("fl_paged_attn_decode", _I, _XP, _PP, _I, _P, _I, _P, _L, _L, _P, _I, _P, _L, _L, _P, _P, _Z, _P)
 
 
-def _flat(t, dtype, device, name, numel=None, at_least=None):
-    """Data pointer of a contiguous tensor of `dtype` on `device` (None stays None)."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _flat(t, dtype, dev, name, numel=-1):
+    """Data pointer of a contiguous tensor of `dtype` on device number `dev` (None stays None)."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if numel is not None and t.numel() != numel:
+    if numel >= 0 and t.numel() != numel:
         raise ValueError(f"{name} must hold {numel} entries, got {t.numel()}")
-    if at_least is not None and t.numel() < at_least:
-        raise ValueError(f"{name} must hold at least {at_least} entries, got {t.numel()}")
     return t.data_ptr()
 
 
-def _rows(t, dtype, device, name, heads):
-    """(pointer, row stride, head stride) of [n][heads][128] with contiguous channels."""
+def _rows(t, dtype, dev, name, heads):
+    """(rows, pointer, row stride, head stride) of [n][heads][128] with contiguous channels;
+    heads = 0: any number."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
-        raise ValueError(f"{name} must be [n][{heads}][{HEAD_DIM}] with contiguous channels")
-    n, h = t.shape[0], heads
-    return t.data_ptr(), t.stride(0) if n > 1 else h * HEAD_DIM, t.stride(1) if h > 1 else HEAD_DIM
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}, got {t.device}")
+    shape = t.shape
+    if len(shape) != 3 or (heads and shape[1] != heads) or shape[2] != HEAD_DIM:
+        raise ValueError(f"{name} must be [n][{heads or 'heads'}][{HEAD_DIM}], got {list(shape)}")
+    n, h = shape[0], shape[1]
+    rs, hs, cs = t.stride()
+    if cs != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    return n, t.data_ptr(), rs if n > 1 else h * HEAD_DIM, hs if h > 1 else HEAD_DIM
 
 
-def _call(where, device, stream, fn, *args):
-    """fn(*args, stream) with `device` current; raises FlashLoopError unless FL_OK."""
-    i = device.index
+def _call(where, dev, stream, fn, *args):
+    """fn(*args, stream) with device number `dev` current; raises FlashLoopError unless FL_OK."""
     if stream is None:
-        stream = torch.cuda.current_stream(i).cuda_stream
+        stream = _raw_stream(dev)
     elif isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == i:
+    if _current_device() == dev:
         st = fn(*args, stream)
     else:
-        with torch.cuda.device(i):
+        with torch.cuda.device(dev):
             st = fn(*args, stream)
-    if st != abi.FL_OK:
+    if st:
         raise FlashLoopError(where, st)
 
 
@@ -113,14 +117,14 @@ class PagedIndex:
     def __init__(self, table, length, free_pages, n_free, status=None):
         if not isinstance(table, torch.Tensor) or table.dim() != 2:
             raise ValueError("table must be [slots][max_pages]")
-        self.device = table.device
-        i32 = torch.int32
+        self.device, self.dev = table.device, table.get_device()
+        i32, dev = torch.int32, self.dev
         self.slots, self.max_pages, self.pages = table.shape[0], table.shape[1], free_pages.numel()
         self.table, self.length, self.free_pages, self.n_free, self.status = table, length, free_pages, n_free, status
         self.c = fl_paged_index(
-            _flat(table, i32, self.device, "table"), _flat(length, i32, self.device, "length", self.slots),
-            _flat(free_pages, i32, self.device, "free_pages"), _flat(n_free, i32, self.device, "n_free", 1),
-            _flat(status, i32, self.device, "status", at_least=3), self.slots, self.max_pages, self.pages)
+            _flat(table, i32, dev, "table"), _flat(length, i32, dev, "length", self.slots),
+            _flat(free_pages, i32, dev, "free_pages"), _flat(n_free, i32, dev, "n_free", 1),
+            _flat(status, i32, dev, "status", 3), self.slots, self.max_pages, self.pages)
         self.ref = ctypes.byref(self.c)
 
     @classmethod
@@ -139,7 +143,7 @@ class PagedPool:
     def __init__(self, rec, tail_k, tail_v):
         if not isinstance(rec, torch.Tensor) or rec.dim() != 3 or rec.shape[2] != GROUP_RECORD:
             raise ValueError(f"rec must be [pages][kv_heads][{GROUP_RECORD}]")
-        self.device = rec.device
+        self.device, self.dev = rec.device, rec.get_device()
         self.pages, self.kv_heads = rec.shape[0], rec.shape[1]
         for t, name in ((tail_k, "tail_k"), (tail_v, "tail_v")):
             if not isinstance(t, torch.Tensor) or t.dim() != 4 or tuple(t.shape[1:]) != (self.kv_heads, PAGE, HEAD_DIM):
@@ -148,10 +152,10 @@ class PagedPool:
             raise ValueError("tail_k and tail_v must have the same shape")
         self.slots = tail_k.shape[0]
         self.rec, self.tail_k, self.tail_v = rec, tail_k, tail_v
-        bf16 = torch.bfloat16
+        bf16, dev = torch.bfloat16, self.dev
         self.c = fl_paged_pool(
-            _flat(rec, torch.uint8, self.device, "rec"), _flat(tail_k, bf16, self.device, "tail_k"),
-            _flat(tail_v, bf16, self.device, "tail_v"), self.kv_heads, HEAD_DIM, PAGE)
+            _flat(rec, torch.uint8, dev, "rec"), _flat(tail_k, bf16, dev, "tail_k"),
+            _flat(tail_v, bf16, dev, "tail_v"), self.kv_heads, HEAD_DIM, PAGE)
         self.ref = ctypes.byref(self.c)
 
     @classmethod
@@ -166,14 +170,15 @@ class PagedPool:
 def _fit(index, pool):
     if pool.pages < index.pages or pool.slots < index.slots:
         raise ValueError("the pool must hold the index's pages and slots")
-    if pool.device != index.device:
+    if pool.dev != index.dev:
         raise ValueError("index and pool must be on one device")
 
 
-def _batch(index, slots, batch=None):
+def _named(index, slots, batch=None):
+    """(batch, pointer) of the named slots; None names rows 0 .. batch - 1 (all by default)."""
     if slots is None:
         return index.slots if batch is None else batch, None
-    p = _flat(slots, torch.int32, index.device, "slots")
+    p = _flat(slots, torch.int32, index.dev, "slots")
     n = slots.numel()
     if batch is not None and n != batch:
         raise ValueError(f"slots must hold one entry per batch row ({batch}), got {n}")
@@ -181,59 +186,65 @@ def _batch(index, slots, batch=None):
 
 
 def fl_paged_index_init(index, stream=None):
-    _call("fl_paged_index_init", index.device, stream, _c_index_init, index.ref)
+    _call("fl_paged_index_init", index.dev, stream, _c_index_init, index.ref)
 
 
 def fl_paged_extend(index, slots, n_new, start, cu, stream=None):
     """Lengths += n_new (int32 [batch]); start (int32 [batch]) and cu (int32 [batch + 1]) are
     written: where the new tokens begin (-1: padded or refused) and their input rows."""
-    dev, i32 = index.device, torch.int32
-    n, sp = _batch(index, slots, n_new.numel())
-    _call("fl_paged_extend", dev, stream, _c_extend, index.ref, n, sp, _flat(n_new, i32, dev, "n_new"),
-          _flat(start, i32, dev, "start", n), _flat(cu, i32, dev, "cu", n + 1))
+    dev, i32 = index.dev, torch.int32
+    np = _flat(n_new, i32, dev, "n_new")
+    n, sp = _named(index, slots, n_new.numel())
+    _call("fl_paged_extend", dev, stream, _c_extend, index.ref, n, sp, np, _flat(start, i32, dev, "start", n),
+          _flat(cu, i32, dev, "cu", n + 1))
 
 
 def fl_paged_release(index, slots, stream=None):
-    n, sp = _batch(index, slots)
-    _call("fl_paged_release", index.device, stream, _c_release, index.ref, n, sp)
+    n, sp = _named(index, slots)
+    _call("fl_paged_release", index.dev, stream, _c_release, index.ref, n, sp)
 
 
 def fl_paged_slot_map(index, slots, start, cu, place, pos, stream=None):
     """Place and position (int32 [n_tokens], either may be None) of tokens start[i] .. of the
     entries' rows cu[i] .. cu[i + 1] - 1."""
-    dev, i32 = index.device, torch.int32
-    n, sp = _batch(index, slots, start.numel())
+    dev, i32 = index.dev, torch.int32
+    tp = _flat(start, i32, dev, "start")
+    n, sp = _named(index, slots, start.numel())
     out = place if place is not None else pos
     t = 0 if out is None else out.numel()
-    _call("fl_paged_slot_map", dev, stream, _c_slot_map, index.ref, n, sp, _flat(start, i32, dev, "start"),
-          _flat(cu, i32, dev, "cu", n + 1), t, _flat(place, i32, dev, "place", t), _flat(pos, i32, dev, "pos", t))
+    _call("fl_paged_slot_map", dev, stream, _c_slot_map, index.ref, n, sp, tp, _flat(cu, i32, dev, "cu", n + 1), t,
+          _flat(place, i32, dev, "place", t), _flat(pos, i32, dev, "pos", t))
+
+
+def _pair(k, v, dev, heads):
+    """(rows, k, v, row stride, head stride) of keys and values that are laid out alike."""
+    n, kp, ts, hs = _rows(k, torch.bfloat16, dev, "k", heads)
+    m, vp, vts, vhs = _rows(v, torch.bfloat16, dev, "v", heads)
+    if n != m or ts != vts or hs != vhs:
+        raise ValueError("k and v must have the same shape and strides")
+    return n, kp, vp, ts, hs
 
 
 def fl_paged_append(index, pool, slots, start, cu, k, v, stream=None):
     """k, v: BF16 [n_tokens][kv_heads][128] (contiguous channels, the same strides): rows
     cu[i] .. cu[i + 1] - 1 are tokens start[i] .. of request i (fl_paged_extend's)."""
     _fit(index, pool)
-    dev, i32 = index.device, torch.int32
-    n, sp = _batch(index, slots, start.numel())
-    kp, ts, hs = _rows(k, torch.bfloat16, dev, "k", pool.kv_heads)
-    vp, vts, vhs = _rows(v, torch.bfloat16, dev, "v", pool.kv_heads)
-    if k.shape != v.shape or (ts, hs) != (vts, vhs):
-        raise ValueError("k and v must have the same shape and strides")
-    _call("fl_paged_append", dev, stream, _c_append, index.ref, pool.ref, n, sp, _flat(start, i32, dev, "start"),
-          _flat(cu, i32, dev, "cu", n + 1), k.shape[0], kp, vp, ts, hs)
+    dev, i32 = index.dev, torch.int32
+    tp = _flat(start, i32, dev, "start")
+    n, sp = _named(index, slots, start.numel())
+    rows, kp, vp, ts, hs = _pair(k, v, dev, pool.kv_heads)
+    _call("fl_paged_append", dev, stream, _c_append, index.ref, pool.ref, n, sp, tp, _flat(cu, i32, dev, "cu", n + 1),
+          rows, kp, vp, ts, hs)
 
 
 def fl_paged_read(index, pool, place, k, v, stream=None):
     """k, v: BF16 [n_tokens][kv_heads][128], row t receives the token at place[t] (int32; -1:
     left as it was)."""
     _fit(index, pool)
-    dev = index.device
-    kp, ts, hs = _rows(k, torch.bfloat16, dev, "k", pool.kv_heads)
-    vp, vts, vhs = _rows(v, torch.bfloat16, dev, "v", pool.kv_heads)
-    if k.shape != v.shape or (ts, hs) != (vts, vhs):
-        raise ValueError("k and v must have the same shape and strides")
-    _call("fl_paged_read", dev, stream, _c_read, index.ref, pool.ref, k.shape[0],
-          _flat(place, torch.int32, dev, "place", k.shape[0]), kp, vp, ts, hs)
+    dev = index.dev
+    rows, kp, vp, ts, hs = _pair(k, v, dev, pool.kv_heads)
+    _call("fl_paged_read", dev, stream, _c_read, index.ref, pool.ref, rows, _flat(place, torch.int32, dev, "place", rows),
+          kp, vp, ts, hs)
 
 
 def fl_paged_workspace_bytes(index, pool, batch: int, q_heads: int) -> int:
@@ -241,7 +252,8 @@ def fl_paged_workspace_bytes(index, pool, batch: int, q_heads: int) -> int:
 
 
 def fl_paged_workspace_init(ws, stream=None):
-    _call("fl_paged_workspace_init", ws.device, stream, _c_ws_init, _flat(ws, torch.uint8, None, "ws"), ws.numel())
+    dev = ws.get_device()
+    _call("fl_paged_workspace_init", dev, stream, _c_ws_init, _flat(ws, torch.uint8, dev, "ws"), ws.numel())
 
 
 def workspace(index, pool, batch: int, q_heads: int, stream=None) -> torch.Tensor:
@@ -256,18 +268,24 @@ def workspace(index, pool, batch: int, q_heads: int, stream=None) -> torch.Tenso
     return ws
 
 
+def _selection(sel, dev, n, kv_heads):
+    """(keep, pointer) of a selection [n][kv_heads][keep]."""
+    p = _flat(sel, torch.int32, dev, "sel")
+    if sel.dim() != 3 or sel.shape[0] != n or sel.shape[1] != kv_heads:
+        raise ValueError(f"sel must be [{n}][{kv_heads}][keep]")
+    return sel.shape[2], p
+
+
 def fl_paged_select(index, pool, slots, q, sel, ws, stream=None):
     """q: BF16 [batch][q_heads][128]; sel: int32 [batch][kv_heads][keep] receives the blocks of
     the highest score, ascending, -1 behind the last."""
     _fit(index, pool)
-    dev = index.device
-    heads = q.shape[1] if q.dim() == 3 else 0
-    qp, qb, qh = _rows(q, torch.bfloat16, dev, "q", heads)
-    n, sp = _batch(index, slots, q.shape[0])
-    if sel.dim() != 3 or sel.shape[0] != n or sel.shape[1] != pool.kv_heads:
-        raise ValueError(f"sel must be [{n}][{pool.kv_heads}][keep]")
-    _call("fl_paged_select", dev, stream, _c_select, index.ref, pool.ref, n, sp, heads, qp, qb, qh, sel.shape[2],
-          _flat(sel, torch.int32, dev, "sel"), _flat(ws, torch.uint8, dev, "ws"), ws.numel())
+    dev = index.dev
+    n, qp, qb, qh = _rows(q, torch.bfloat16, dev, "q", 0)
+    _, sp = _named(index, slots, n)
+    keep, selp = _selection(sel, dev, n, pool.kv_heads)
+    _call("fl_paged_select", dev, stream, _c_select, index.ref, pool.ref, n, sp, q.shape[1], qp, qb, qh, keep, selp,
+          _flat(ws, torch.uint8, dev, "ws"), ws.numel())
 
 
 def fl_paged_attn_decode(index, pool, slots, q, o, ws, lse=None, sel=None, stream=None):
@@ -275,21 +293,16 @@ def fl_paged_attn_decode(index, pool, slots, q, o, ws, lse=None, sel=None, strea
     cache, or over the blocks of sel (int32 [batch][kv_heads][keep]) and the tail; lse: None or
     fp32 [batch][q_heads] (base 2)."""
     _fit(index, pool)
-    dev = index.device
-    heads = q.shape[1] if q.dim() == 3 else 0
-    qp, qb, qh = _rows(q, torch.bfloat16, dev, "q", heads)
-    op, ob, oh = _rows(o, torch.float32, dev, "o", heads)
-    n, sp = _batch(index, slots, q.shape[0])
-    if o.shape[0] != n:
+    dev = index.dev
+    n, qp, qb, qh = _rows(q, torch.bfloat16, dev, "q", 0)
+    heads = q.shape[1]
+    m, op, ob, oh = _rows(o, torch.float32, dev, "o", heads)
+    if m != n:
         raise ValueError("o must have q's shape")
-    keep = 0
-    if sel is not None:
-        if sel.dim() != 3 or sel.shape[0] != n or sel.shape[1] != pool.kv_heads:
-            raise ValueError(f"sel must be [{n}][{pool.kv_heads}][keep]")
-        keep = sel.shape[2]
-    _call("fl_paged_attn_decode", dev, stream, _c_attn, index.ref, pool.ref, n, sp, heads, qp, qb, qh,
-          _flat(sel, torch.int32, dev, "sel"), keep, op, ob, oh, _flat(lse, torch.float32, dev, "lse", n * heads),
-          _flat(ws, torch.uint8, dev, "ws"), ws.numel())
+    _, sp = _named(index, slots, n)
+    keep, selp = (0, None) if sel is None else _selection(sel, dev, n, pool.kv_heads)
+    _call("fl_paged_attn_decode", dev, stream, _c_attn, index.ref, pool.ref, n, sp, heads, qp, qb, qh, selp, keep, op, ob,
+          oh, _flat(lse, torch.float32, dev, "lse", n * heads), _flat(ws, torch.uint8, dev, "ws"), ws.numel())
 
 
 class PagedCache:
