@@ -5,14 +5,15 @@
 // ceil(c_i / 64); with P_i the sum of need over the valid entries up to i, entry i is granted
 // when need_i = 0 or P_i <= n_free, and its pages are free[n_free - 1 - (P_i - need_i) - j].
 // The granted entries that need pages are a prefix of the valid ones that do, so the stack
-// simply loses its top P.  One block does it: the work is a scan over at most 8192 entries
-// and 8 bytes per page, and its time is the launch and four dependent trips to memory.
+// simply loses its top P and every entry's place on it is P_i - need_i.  One block does it (of
+// 128 threads up to 128 entries, where its barriers cost half of 1024 threads'): the work is a
+// scan over at most 8192 entries and 8 bytes per page, and its time is the launch and four
+// dependent trips to memory.  The kernels here start while their predecessor ends (programmatic
+// launch) and wait for it before they touch memory.
 #include "paged.cuh"
 
 namespace fl {
 namespace {
-
-constexpr int kT = 1024;
 
 __global__ void index_init_kernel(fl_paged_index x) {
   const int64_t n = (int64_t)x.slots * x.max_pages, step = (int64_t)gridDim.x * blockDim.x;
@@ -25,56 +26,100 @@ __global__ void index_init_kernel(fl_paged_index x) {
 }
 
 // One bit per slot (dynamic shared memory), set once the slot has been named.
+template <int kT>
 struct Claims {
   uint32_t* bits;
   int32_t* slot;  // [kT] of this chunk
 
+  // Before the first chunk; the caller's next barrier comes before any use.
   __device__ void clear(int slots) {
     for (int i = threadIdx.x; i < (slots + 31) / 32; i += kT) bits[i] = 0u;
-    __syncthreads();
   }
   // True for the entry that names its slot first (s < 0: no slot); all threads call it, one
   // chunk of kT entries after the other.
   __device__ bool first(int s) {
-    const bool earlier = s >= 0 && ((bits[s >> 5] >> (s & 31)) & 1u);
+    const uint32_t bit = s >= 0 ? 1u << (s & 31) : 0u;
+    __syncthreads();
+    const bool earlier = s >= 0 && (bits[s >> 5] & bit);
     slot[threadIdx.x] = s;
     __syncthreads();
-    bool twice = false;
-    if (s >= 0) twice = (atomicOr(&bits[s >> 5], 1u << (s & 31)) >> (s & 31)) & 1u;
+    const bool twice = s >= 0 && (atomicOr(&bits[s >> 5], bit) & bit);
     bool mine = s >= 0 && !earlier;
     if (__syncthreads_or(twice && !earlier)) {
       // rare: some slot stands twice in this chunk, the first one counts
       for (int i = 0; i < (int)threadIdx.x && mine; ++i) mine = slot[i] != s;
-      __syncthreads();
     }
     return mine;
   }
 };
 
-struct PageJobs {  // of one chunk: entry t moves pages [before[t], before[t] + count)
+// Two sums at once: `v`'s halves (below 2^32 each in total).
+template <int kT>
+__device__ __forceinline__ uint64_t scan_pair(uint64_t v, uint64_t* red, uint64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) red[warp] = x;
+  __syncthreads();
+  uint64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kT / 32; ++w) {
+    const uint64_t r = red[w];
+    before += w < warp ? r : 0;
+    total += r;
+  }
+  __syncthreads();
+  return before + x - v;
+}
+
+// One chunk's pages to move: entry t's are jobs [before[t], before[t + 1]), page j of them goes
+// with block block0[t] + (job) of its slot.  Four jobs a thread are in flight at once.
+template <int kT>
+struct Jobs {
   int32_t before[kT + 1], slot[kT], block0[kT];
+
+  template <class F>
+  __device__ void run(F&& move) const {
+    const int n = before[kT];
+    for (int i0 = threadIdx.x; i0 < n; i0 += 4 * kT) {
+      int t[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) t[y] = i0 + y * kT < n ? paged_find(before, kT, i0 + y * kT) : -1;
+      move(t, i0);
+    }
+  }
 };
 
+template <int kT>
 __global__ void __launch_bounds__(kT) extend_kernel(fl_paged_index x, int batch, const int32_t* slots,
                                                     const int32_t* n_new, int32_t* start, int32_t* cu) {
   extern __shared__ uint32_t s_bits[];
-  __shared__ PageJobs jobs;
   __shared__ int32_t s_slot[kT];
-  __shared__ int red[kT / 32];
+  __shared__ uint64_t red[kT / 32];
+  __shared__ int s_taken;
+  __shared__ Jobs<kT> jobs;
   const int tid = threadIdx.x;
-  Claims claims{s_bits, s_slot};
+  Claims<kT> claims{s_bits, s_slot};
   claims.clear(x.slots);
+  if (tid == 0) s_taken = 0;
+  grid_dep_launch();
+  grid_dep_wait();
   const int n_free = min(max(*x.n_free, 0), x.pages);
-  int run_tokens = 0, run_pages = 0, taken = 0;
+  uint64_t run = 0;  // tokens, and pages needed in the high half (2^27 at most)
   for (int b0 = 0; b0 < batch; b0 += kT) {
     const int b = b0 + tid;
     int s = -1, n = 0, c = 0, need = 0;
     if (b < batch) {
+      n = n_new[b];
       s = paged_slot(x, slots, b, true);
-      n = __ldg(n_new + b);
+      if (s >= 0) c = x.length[s];
     }
-    const bool named = s >= 0;
-    const bool mine = claims.first(s);
+    const bool named = s >= 0, mine = claims.first(s);
     if (named && !mine) paged_error(x, FL_DEV_SLOT_TWICE, b);
     if (!mine) s = -1;
     if (s >= 0 && n < 0) {
@@ -82,7 +127,6 @@ __global__ void __launch_bounds__(kT) extend_kernel(fl_paged_index x, int batch,
       s = -1;
     }
     if (s >= 0) {
-      c = x.length[s];
       if (c < 0 || (int64_t)c + n > (int64_t)x.max_pages * FL_PAGE) {
         paged_error(x, FL_DEV_TOO_LONG, b);
         s = -1;
@@ -90,114 +134,170 @@ __global__ void __launch_bounds__(kT) extend_kernel(fl_paged_index x, int batch,
         need = ((c + n + FL_PAGE - 1) >> 6) - ((c + FL_PAGE - 1) >> 6);
       }
     }
-    int total_tokens, total_pages;
-    const int tok = run_tokens + paged_block_scan<kT>(max(n, 0), red, total_tokens);
-    // at most FL_PAGED_MAX_BLOCKS pages an entry: 2^27 in all
-    const int before = run_pages + paged_block_scan<kT>(need, red, total_pages);
-    const bool granted = s >= 0 && (need == 0 || before + need <= n_free);
+    uint64_t total;
+    const uint64_t before = run + scan_pair<kT>((uint64_t)need << 32 | (uint32_t)max(n, 0), red, total);
+    const int at = (int)(before >> 32);
+    const bool granted = s >= 0 && (need == 0 || at + need <= n_free);
     if (s >= 0 && !granted) paged_error(x, FL_DEV_NO_PAGE, b);
     if (b < batch) {
       start[b] = granted ? c : -1;
-      cu[b] = tok;
+      cu[b] = (int)(uint32_t)before;
     }
     if (granted) x.length[s] = c + n;
     const int count = granted ? need : 0;
-    int n_jobs;
-    const int at = paged_block_scan<kT>(count, red, n_jobs);
-    jobs.before[tid] = at;
-    jobs.slot[tid] = s;
-    jobs.block0[tid] = ((c + FL_PAGE - 1) >> 6) - at;
-    if (tid == 0) jobs.before[kT] = n_jobs;
-    __syncthreads();
-    // the granted entries' pages are consecutive on the stack, from `taken` on
-    for (int i = tid; i < n_jobs; i += kT) {
-      const int t = paged_find(jobs.before, kT, i);
-      x.table[(int64_t)jobs.slot[t] * x.max_pages + jobs.block0[t] + i] = x.free_pages[n_free - 1 - taken - i];
+    if (count > 0) atomicMax(&s_taken, at + count);
+    const int block0 = (c + FL_PAGE - 1) >> 6;
+    if (!__syncthreads_or(count > 1)) {
+      // a decode step: a page a request at most
+      if (count == 1) x.table[(int64_t)s * x.max_pages + block0] = x.free_pages[n_free - 1 - at];
+    } else {
+      // the granted entries' pages lie one behind the other on the stack, from `base` on
+      const int base = (int)(run >> 32), taken = max(s_taken - base, 0);
+      jobs.before[tid] = min(at - base, taken);
+      jobs.slot[tid] = s;
+      jobs.block0[tid] = block0 - (at - base);
+      if (tid == 0) jobs.before[kT] = taken;
+      __syncthreads();
+      jobs.run([&](const int (&t)[4], int i0) {
+        int page[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) page[y] = t[y] >= 0 ? x.free_pages[n_free - 1 - base - (i0 + y * kT)] : 0;
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (t[y] >= 0) x.table[(int64_t)jobs.slot[t[y]] * x.max_pages + jobs.block0[t[y]] + i0 + y * kT] = page[y];
+      });
+      __syncthreads();
     }
-    taken += n_jobs;
-    run_tokens += total_tokens;
-    run_pages += total_pages;
-    __syncthreads();
+    run += total;
   }
+  __syncthreads();
   if (tid == 0) {
-    cu[batch] = run_tokens;
-    *x.n_free = n_free - taken;
+    cu[batch] = (int)(uint32_t)run;
+    *x.n_free = n_free - s_taken;
   }
 }
 
+template <int kT>
 __global__ void __launch_bounds__(kT) release_kernel(fl_paged_index x, int batch, const int32_t* slots) {
   extern __shared__ uint32_t s_bits[];
-  __shared__ PageJobs jobs;
   __shared__ int32_t s_slot[kT];
-  __shared__ int red[kT / 32];
+  __shared__ uint64_t red[kT / 32];
+  __shared__ Jobs<kT> jobs;
   const int tid = threadIdx.x;
-  Claims claims{s_bits, s_slot};
+  Claims<kT> claims{s_bits, s_slot};
   claims.clear(x.slots);
+  grid_dep_launch();
+  grid_dep_wait();
   const int n_free = min(max(*x.n_free, 0), x.pages);
-  int given = 0;
+  uint64_t given = 0;  // 2^27 at most
   for (int b0 = 0; b0 < batch; b0 += kT) {
     const int b = b0 + tid;
-    int s = b < batch ? paged_slot(x, slots, b, true) : -1;
-    const bool named = s >= 0;
+    const int s = b < batch ? paged_slot(x, slots, b, true) : -1;
+    int count = s >= 0 ? (paged_length(x, s, b, true) + FL_PAGE - 1) >> 6 : 0;
     const bool mine = claims.first(s);
-    if (named && !mine) paged_error(x, FL_DEV_SLOT_TWICE, b);
-    int count = 0;
-    if (mine) {
-      count = (paged_length(x, s, b, true) + FL_PAGE - 1) >> 6;
-      x.length[s] = 0;
-    }
-    int n_jobs;
-    const int at = paged_block_scan<kT>(count, red, n_jobs);
+    if (s >= 0 && !mine) paged_error(x, FL_DEV_SLOT_TWICE, b);
+    if (!mine) count = 0;
+    if (mine) x.length[s] = 0;
+    uint64_t total;
+    const int at = (int)scan_pair<kT>((uint64_t)count, red, total);
     jobs.before[tid] = at;
     jobs.slot[tid] = s;
     jobs.block0[tid] = -at;
-    if (tid == 0) jobs.before[kT] = n_jobs;
+    if (tid == 0) jobs.before[kT] = (int)total;
     __syncthreads();
-    for (int i = tid; i < n_jobs; i += kT) {
-      const int t = paged_find(jobs.before, kT, i);
-      int32_t* e = x.table + (int64_t)jobs.slot[t] * x.max_pages + jobs.block0[t] + i;
-      const int page = *e;
-      *e = -1;
-      if (page < 0 || page >= x.pages) paged_error(x, FL_DEV_PAGE_RANGE, b0 + t);
-      // a stack that would grow beyond `pages` has been handed pages that are free already
-      if (n_free + given + i < x.pages) x.free_pages[n_free + given + i] = page;
-      else paged_error(x, FL_DEV_PAGE_RANGE, b0 + t);
-    }
-    given += n_jobs;
+    const int64_t top = n_free + (int64_t)given;
+    jobs.run([&](const int (&t)[4], int i0) {
+      int page[4];
+      int32_t* e[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        if (t[y] < 0) continue;
+        e[y] = x.table + (int64_t)jobs.slot[t[y]] * x.max_pages + jobs.block0[t[y]] + i0 + y * kT;
+        page[y] = *e[y];
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        if (t[y] < 0) continue;
+        const int64_t to = top + i0 + y * kT;
+        *e[y] = -1;
+        // a stack that would grow beyond `pages` has been handed pages that are free already
+        if (page[y] < 0 || page[y] >= x.pages || to >= x.pages) paged_error(x, FL_DEV_PAGE_RANGE, b0 + t[y]);
+        if (to < x.pages) x.free_pages[to] = page[y];
+      }
+    });
     __syncthreads();
+    given += total;
   }
-  if (tid == 0) *x.n_free = min(n_free + given, x.pages);
+  __syncthreads();
+  if (tid == 0) *x.n_free = (int)min((int64_t)n_free + (int64_t)given, (int64_t)x.pages);
 }
 
-__global__ void __launch_bounds__(256) slot_map_kernel(fl_paged_index x, int batch, const int32_t* slots,
-                                                       const int32_t* start, const int32_t* cu, int n_tokens,
-                                                       int32_t* place, int32_t* pos) {
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t >= n_tokens || t < __ldg(cu) || t >= __ldg(cu + batch)) return;
-  int lo = 0, hi = batch;  // cu[lo] <= t < cu[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(cu + mid) <= t) lo = mid;
-    else hi = mid;
+// Four consecutive rows a thread; the offsets are searched in shared memory where they fit.
+constexpr int kMapT = 256, kMapRows = 4, kMapHeld = 2048;
+
+__global__ void __launch_bounds__(kMapT) slot_map_kernel(fl_paged_index x, int batch, const int32_t* slots,
+                                                         const int32_t* start, const int32_t* cu, int n_tokens,
+                                                         int32_t* place, int32_t* pos, int vec) {
+  __shared__ int32_t s_cu[kMapHeld + 1];
+  grid_dep_launch();
+  grid_dep_wait();
+  const bool held = batch <= kMapHeld;
+  if (held) {
+    for (int i = threadIdx.x; i <= batch; i += kMapT) s_cu[i] = cu[i];
+    __syncthreads();
   }
-  const int s = paged_slot(x, slots, lo, t == __ldg(cu + lo));
-  const int begin = __ldg(start + lo), first = __ldg(cu + lo);
-  int at = -1, where = -1;
-  if (s >= 0 && begin >= 0 && first >= 0 && begin <= INT32_MAX - (t - first)) {
-    at = begin + (t - first);
-    const int n = paged_length(x, s, lo, t == first), full = paged_full(n);
-    if (at < n) {
-      const int block = at >> 6;
-      int page = block < full ? x.table[(int64_t)s * x.max_pages + block] : x.pages + s;
-      if (page < 0 || (block < full && page >= x.pages)) {
-        paged_error(x, FL_DEV_PAGE_RANGE, lo);
-        page = -1;
+  const int32_t* off = held ? s_cu : cu;
+  const int t0 = (blockIdx.x * kMapT + threadIdx.x) * kMapRows;
+  const int begin = off[0], end = min(off[batch], n_tokens);
+  if (t0 + kMapRows <= begin || t0 >= end) return;
+  int at[kMapRows], where[kMapRows];
+  int b = -1, first = 0, last = -1;  // rows [first, last) are entry b's
+  int s = -1, from = -1, n = 0, full = 0;
+#pragma unroll
+  for (int y = 0; y < kMapRows; ++y) {
+    const int t = t0 + y;
+    at[y] = where[y] = -1;
+    if (t < begin || t >= end) continue;
+    if (t >= last || t < first) {
+      int lo = 0, hi = batch;  // off[lo] <= t < off[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off[mid] <= t) lo = mid;
+        else hi = mid;
       }
-      where = page < 0 ? -1 : page * FL_PAGE + (at & 63);
+      b = lo;
+      first = off[b];
+      last = off[b + 1];
+      s = paged_slot(x, slots, b, t == first);
+      from = start[b];
+      n = s >= 0 ? paged_length(x, s, b, t == first) : 0;
+      full = paged_full(n);
     }
+    if (s < 0 || from < 0 || from > INT32_MAX - (t - first)) continue;
+    at[y] = from + (t - first);
+    if (at[y] >= n) continue;
+    const int block = at[y] >> 6;
+    int page = x.pages + s;
+    if (block < full) {
+      page = x.table[(int64_t)s * x.max_pages + block];
+      if (page < 0 || page >= x.pages) {
+        paged_error(x, FL_DEV_PAGE_RANGE, b);
+        continue;
+      }
+    }
+    where[y] = page * FL_PAGE + (at[y] & 63);
   }
-  if (place) place[t] = where;
-  if (pos) pos[t] = at;
+  if (vec && t0 >= begin && t0 + kMapRows <= end) {
+    if (place) *reinterpret_cast<int4*>(place + t0) = make_int4(where[0], where[1], where[2], where[3]);
+    if (pos) *reinterpret_cast<int4*>(pos + t0) = make_int4(at[0], at[1], at[2], at[3]);
+    return;
+  }
+#pragma unroll
+  for (int y = 0; y < kMapRows; ++y) {
+    if (t0 + y < begin || t0 + y >= end) continue;
+    if (place) place[t0 + y] = where[y];
+    if (pos) pos[t0 + y] = at[y];
+  }
 }
 
 }  // namespace
@@ -209,20 +309,23 @@ cudaError_t launch_paged_index_init(const fl_paged_index& x, cudaStream_t s) {
 
 cudaError_t launch_paged_extend(const fl_paged_index& x, int batch, const int32_t* slots, const int32_t* n_new,
                                 int32_t* start, int32_t* cu, cudaStream_t s) {
-  extend_kernel<<<1, kT, (size_t)(x.slots + 31) / 32 * 4, s>>>(x, batch, slots, n_new, start, cu);
-  return cudaGetLastError();
+  const size_t bits = (size_t)(x.slots + 31) / 32 * 4;
+  if (batch <= 128) return launch_pdl(extend_kernel<128>, dim3(1), dim3(128), bits, s, x, batch, slots, n_new, start, cu);
+  return launch_pdl(extend_kernel<1024>, dim3(1), dim3(1024), bits, s, x, batch, slots, n_new, start, cu);
 }
 
 cudaError_t launch_paged_release(const fl_paged_index& x, int batch, const int32_t* slots, cudaStream_t s) {
-  release_kernel<<<1, kT, (size_t)(x.slots + 31) / 32 * 4, s>>>(x, batch, slots);
-  return cudaGetLastError();
+  const size_t bits = (size_t)(x.slots + 31) / 32 * 4;
+  if (batch <= 128) return launch_pdl(release_kernel<128>, dim3(1), dim3(128), bits, s, x, batch, slots);
+  return launch_pdl(release_kernel<1024>, dim3(1), dim3(1024), bits, s, x, batch, slots);
 }
 
 cudaError_t launch_paged_slot_map(const fl_paged_index& x, int batch, const int32_t* slots, const int32_t* start,
                                   const int32_t* cu, int n_tokens, int32_t* place, int32_t* pos, cudaStream_t s) {
   if (n_tokens == 0) return cudaSuccess;
-  slot_map_kernel<<<(n_tokens + 255) / 256, 256, 0, s>>>(x, batch, slots, start, cu, n_tokens, place, pos);
-  return cudaGetLastError();
+  const int vec = (reinterpret_cast<uintptr_t>(place) | reinterpret_cast<uintptr_t>(pos)) % 16 == 0;
+  const unsigned grid = (unsigned)(((int64_t)n_tokens + kMapT * kMapRows - 1) / (kMapT * kMapRows));
+  return launch_pdl(slot_map_kernel, dim3(grid), dim3(kMapT), 0, s, x, batch, slots, start, cu, n_tokens, place, pos, vec);
 }
 
 }  // namespace fl
