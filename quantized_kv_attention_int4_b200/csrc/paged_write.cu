@@ -7,10 +7,10 @@ namespace fl {
 namespace {
 
 // ---- append -----------------------------------------------------------------------------
-// An item is one block of one request that fills up (or, for a request none of whose blocks
-// fills up, its tail alone), for one head.  The item of a request's first block also writes
-// its new tail rows: that block is the only one whose older rows lie in the tail, so the CTA
-// has them in registers before it overwrites any.
+// A request whose blocks fill up is one item per such block and head; the item of the first one
+// also writes the head's new tail rows: that block is the only one whose older rows lie in the
+// tail, so the CTA has them in registers before it overwrites any.  A request that fills no
+// block (most of a decode step) is one item per 16 heads, a copy of its rows.
 //
 // 256 threads: thread t owns channels 8 (t % 16) .. + 7 of rows t / 16 + 16 i, i = 0..3, of
 // keys and values (16-byte loads, 256-byte rows).  A value group (row, 64-channel half) is
@@ -34,22 +34,29 @@ __device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
-// quant() of quant.cuh with its rounded division taken only near a half: with r = 1 / s
-// rounded, |d r - d / s| <= 1.6e-6 d / s < 3.2e-5 for codes up to 16 (beyond, both clamp), and
-// the rounded quotient is within 2^-20 of d / s, so away from a half by 1e-4 all of them
-// round to the same code.
-__device__ __forceinline__ uint32_t quant_fast(float x, float s, float r, float z) {
-  const float d = __fsub_rn(x, z), t = d * r, n = rintf(t);
-  if (fabsf(t - n) < 0.4999f) return (uint32_t)min(max(__float2int_rn(n), 0), 15);
-  return quant(x, s, z);
-}
-
+// Eight codes: quant() of quant.cuh with its rounded division taken only near a half.  With
+// r = 1 / s rounded, |d r - d / s| <= 1.6e-6 d / s < 3.2e-5 for codes up to 16 (beyond, both
+// clamp), and the rounded quotient is within 2^-20 of d / s, so away from a half by 1e-4 all of
+// them round to the same code.  Rounding is an addition of 1.5 2^23 (conversions are issued at a
+// quarter of its rate): the sum's low bits are the code.  NaN, which an infinity gives, clamps
+// to 0 as there.
 __device__ __forceinline__ uint32_t quant_word(uint4 x, const float2* sz, const float* rcp) {
-  float f[8];
+  constexpr float kMagic = 12582912.f;
+  float f[8], worst = 0.f;
   bf16x8(x, f);
   uint32_t w = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w |= quant_fast(f[e], sz[e].x, rcp[e], sz[e].y) << (4 * e);
+  for (int e = 7; e >= 0; --e) {
+    const float t = fminf(fmaxf(__fsub_rn(f[e], sz[e].y) * rcp[e], 0.f), 15.f);
+    const float up = __fadd_rn(t, kMagic);
+    worst = fmaxf(worst, fabsf(__fsub_rn(t, __fsub_rn(up, kMagic))));
+    w = (w << 4) + (__float_as_uint(up) & 15u);
+  }
+  if (worst >= 0.4999f) {
+    w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w |= quant(f[e], sz[e].x, sz[e].y) << (4 * e);
+  }
   return w;
 }
 
@@ -63,6 +70,9 @@ __global__ void __launch_bounds__(kAT, 4) append_kernel(PagedAppendArgs a) {
   const int heads = a.p.kv_heads;
   const fl_paged_index& x = a.x;
   const bool tell = blockIdx.x == 0;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int copies = (heads + 15) / 16;
   const int items = paged_scan<kAT>(a.batch, prefix, sm.red, [&](int b) {
     const int s = paged_slot(x, a.slots, b, tell);
     const int c = __ldg(a.start + b), r0 = __ldg(a.cu + b), r1 = __ldg(a.cu + b + 1);
@@ -75,20 +85,32 @@ __global__ void __launch_bounds__(kAT, 4) append_kernel(PagedAppendArgs a) {
       if (tell) paged_error(x, FL_DEV_TOO_LONG, b);
       return 0;
     }
-    return max(1, paged_full(c + r1 - r0) - paged_full(c));
+    const int fill = paged_full(c + r1 - r0) - paged_full(c);
+    return fill ? fill * heads : copies;
   });
   const int chunk = tid & 15, r0 = tid >> 4;
-  for (int64_t w = blockIdx.x; w < (int64_t)items * heads; w += gridDim.x) {
-    const int item = (int)(w / heads), h = (int)(w % heads);
-    const int b = paged_find(prefix, a.batch, item), j = item - prefix[b];
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int b = paged_find(prefix, a.batch, item), left = item - prefix[b];
     const int s = paged_slot(x, a.slots, b, false);
     const int c = __ldg(a.start + b), row0 = __ldg(a.cu + b), n = c + __ldg(a.cu + b + 1) - row0;
-    const int full0 = paged_full(c), full1 = paged_full(n), block = full0 + j;
+    const int full0 = paged_full(c), full1 = paged_full(n);
+    if (full0 == full1) {
+      const int h0 = 16 * left, hn = min(16, heads - h0);
+      for (int y = tid; y < (n - c) * hn * 16; y += kAT) {
+        const int at = y & 15, h = h0 + (y >> 4) % hn, r = (y >> 4) / hn;
+        const int64_t from = (int64_t)(row0 + r) * a.token_stride + (int64_t)h * a.head_stride + 8 * at;
+        const size_t to = (((size_t)s * heads + h) * FL_PAGE + (c - full0 * FL_PAGE) + r) * kD + 8 * at;
+        *reinterpret_cast<uint4*>(a.p.tail_k + to) = *reinterpret_cast<const uint4*>(a.k + from);
+        *reinterpret_cast<uint4*>(a.p.tail_v + to) = *reinterpret_cast<const uint4*>(a.v + from);
+      }
+      continue;
+    }
+    const int j = left / heads, h = left - j * heads, block = full0 + j;
     const size_t tail = ((size_t)s * heads + h) * FL_PAGE * kD;
     uint16_t *tk = a.p.tail_k + tail, *tv = a.p.tail_v + tail;
     int page = -1;
     uint4 k4[4], v4[4];
-    if (block < full1) {
+    {
       page = x.table[(int64_t)s * x.max_pages + block];
       if (page < 0 || page >= x.pages) {
         if (tid == 0) paged_error(x, FL_DEV_PAGE_RANGE, b);
@@ -190,8 +212,9 @@ __global__ void __launch_bounds__(kAT, 4) append_kernel(PagedAppendArgs a) {
 
 // ---- read -------------------------------------------------------------------------------
 // One warp takes 16 consecutive rows of one head: lane l owns channels 8 (l % 16) .. + 7 of
-// rows l / 16, l / 16 + 2, ...; the key scales of its channels stay in registers while the
-// page does not change.
+// rows l / 16, l / 16 + 2, ....  Rows of one page in order, the usual case, are read all at once;
+// otherwise one after the other, the key scales staying in registers while the page does not
+// change.
 constexpr int kReadRows = 16, kReadWarps = 8;
 
 __device__ __forceinline__ uint32_t bf2(float a, float b) {
@@ -209,46 +232,72 @@ __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(PagedReadArgs a) 
   const int64_t job = (int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
   const int64_t run = job / heads;
   const int h = (int)(job % heads), t0 = (int)(run * kReadRows);
+  grid_dep_launch();
+  grid_dep_wait();
   if (run * kReadRows >= a.n_tokens) return;
   const int cl = lane & 15, half = lane >> 4;
   const int mine = lane < kReadRows && t0 + lane < a.n_tokens ? __ldg(a.place + t0 + lane) : -1;
   const int page_end = a.x.pages, all_end = a.x.pages + a.x.slots;
-  int cur = -1;
+  const int64_t out = (int64_t)t0 * a.token_stride + (int64_t)h * a.head_stride + 8 * cl;
   float2 ksz[8];
+  auto key_scales = [&](const uint8_t* rec) {
+    const uint4 s0 = ldg_u4(rec + kRecKsz + 32 * cl), s1 = ldg_u4(rec + kRecKsz + 32 * cl + 16);
+    const uint32_t w[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
+    for (int e = 0; e < 8; ++e) ksz[e] = unpack_sz(w[e]);
+  };
+  auto put = [&](int r, uint32_t kw, uint32_t vw, uint32_t vz) {
+    const float2 vsz = unpack_sz(vz);
+    uint4 ko, vo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      (&ko.x)[e] = bf2(fmaf(nib(kw, 2 * e), ksz[2 * e].x, ksz[2 * e].y), fmaf(nib(kw, 2 * e + 1), ksz[2 * e + 1].x, ksz[2 * e + 1].y));
+      (&vo.x)[e] = bf2(fmaf(nib(vw, 2 * e), vsz.x, vsz.y), fmaf(nib(vw, 2 * e + 1), vsz.x, vsz.y));
+    }
+    __stcs(reinterpret_cast<uint4*>(a.k + out + r * a.token_stride), ko);
+    __stcs(reinterpret_cast<uint4*>(a.v + out + r * a.token_stride), vo);
+  };
+  const int at0 = __shfl_sync(kFull, mine, 0), page0 = at0 >> 6;
+  if (at0 >= 0 && page0 < page_end && (at0 & 63) <= FL_PAGE - kReadRows &&
+      __all_sync(kFull, lane >= kReadRows || mine == at0 + lane)) {
+    const uint8_t* rec = a.p.rec + ((size_t)page0 * heads + h) * kRec;
+    const int row0 = (at0 & 63) + half;
+    key_scales(rec);
+    uint32_t kw[kReadRows / 2], vw[kReadRows / 2], vz[kReadRows / 2];
+#pragma unroll
+    for (int i = 0; i < kReadRows / 2; ++i) {
+      const uint32_t* row = reinterpret_cast<const uint32_t*>(rec + (row0 + 2 * i) * 128);
+      kw[i] = __ldg(row + cl);
+      vw[i] = __ldg(row + 16 + cl);
+      vz[i] = __ldg(reinterpret_cast<const uint32_t*>(rec + kRecVsz) + 2 * (row0 + 2 * i) + (cl >> 3));
+    }
+#pragma unroll
+    for (int i = 0; i < kReadRows / 2; ++i) put(2 * i + half, kw[i], vw[i], vz[i]);
+    return;
+  }
+  int cur = -1;
+#pragma unroll 1
   for (int i = 0; i < kReadRows / 2; ++i) {
-    const int at = __shfl_sync(kFull, mine, 2 * i + half);
+    const int r = 2 * i + half;
+    const int at = __shfl_sync(kFull, mine, r);
     const int page = at >> 6, row = at & 63;
     if (at < 0 || page >= all_end) {
-      if (h == 0 && cl == 0 && (at < -1 || page >= all_end)) paged_error(a.x, FL_DEV_PAGE_RANGE, t0 + 2 * i + half);
+      if (h == 0 && cl == 0 && (at < -1 || page >= all_end)) paged_error(a.x, FL_DEV_PAGE_RANGE, t0 + r);
       continue;
     }
-    uint4 ko, vo;
     if (page < page_end) {
       const uint8_t* rec = a.p.rec + ((size_t)page * heads + h) * kRec;
-      const uint32_t kw = __ldg(reinterpret_cast<const uint32_t*>(rec + row * 128) + cl);
-      const uint32_t vw = __ldg(reinterpret_cast<const uint32_t*>(rec + row * 128 + 64) + cl);
-      const float2 vsz = unpack_sz(__ldg(reinterpret_cast<const uint32_t*>(rec + kRecVsz) + 2 * row + (cl >> 3)));
-      if (page != cur) {
-        const uint4 s0 = ldg_u4(rec + kRecKsz + 32 * cl), s1 = ldg_u4(rec + kRecKsz + 32 * cl + 16);
-        const uint32_t w[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ksz[e] = unpack_sz(w[e]);
-        cur = page;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        (&ko.x)[e] = bf2(fmaf(nib(kw, 2 * e), ksz[2 * e].x, ksz[2 * e].y), fmaf(nib(kw, 2 * e + 1), ksz[2 * e + 1].x, ksz[2 * e + 1].y));
-        (&vo.x)[e] = bf2(fmaf(nib(vw, 2 * e), vsz.x, vsz.y), fmaf(nib(vw, 2 * e + 1), vsz.x, vsz.y));
-      }
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(rec + row * 128);
+      const uint32_t kw = __ldg(words + cl), vw = __ldg(words + 16 + cl);
+      const uint32_t vz = __ldg(reinterpret_cast<const uint32_t*>(rec + kRecVsz) + 2 * row + (cl >> 3));
+      if (page != cur) key_scales(rec);
+      cur = page;
+      put(r, kw, vw, vz);
     } else {
       const size_t off = (((size_t)(page - page_end) * heads + h) * FL_PAGE + row) * kD + 8 * cl;
-      ko = ldg_u4(a.p.tail_k + off);
-      vo = ldg_u4(a.p.tail_v + off);
+      __stcs(reinterpret_cast<uint4*>(a.k + out + r * a.token_stride), ldg_u4(a.p.tail_k + off));
+      __stcs(reinterpret_cast<uint4*>(a.v + out + r * a.token_stride), ldg_u4(a.p.tail_v + off));
     }
-    const int64_t off = (int64_t)(t0 + 2 * i + half) * a.token_stride + (int64_t)h * a.head_stride + 8 * cl;
-    *reinterpret_cast<uint4*>(a.k + off) = ko;
-    *reinterpret_cast<uint4*>(a.v + off) = vo;
   }
 }
 
@@ -261,8 +310,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
   // at most one item per entry and one more per 64 tokens
   const int64_t items = ((int64_t)a.batch + a.n_tokens / FL_PAGE) * a.p.kv_heads;
   const int grid = (int)(items < 4 * sms ? items : 4 * sms);
-  append_kernel<<<grid, kAT, (size_t)(a.batch + 1) * 4, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(append_kernel, dim3(grid), dim3(kAT), (size_t)(a.batch + 1) * 4, s, a);
 }
 
 cudaError_t launch_paged_read(const PagedReadArgs& a, cudaStream_t s) {
@@ -270,8 +318,7 @@ cudaError_t launch_paged_read(const PagedReadArgs& a, cudaStream_t s) {
   const int64_t jobs = ((int64_t)a.n_tokens + kReadRows - 1) / kReadRows * a.p.kv_heads;
   const int64_t grid = (jobs + kReadWarps - 1) / kReadWarps;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  read_kernel<<<(unsigned)grid, kReadWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(read_kernel, dim3((unsigned)grid), dim3(kReadWarps * 32), 0, s, a);
 }
 
 }  // namespace fl
