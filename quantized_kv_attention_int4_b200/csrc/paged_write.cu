@@ -34,13 +34,24 @@ __device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
-// Eight codes: quant() of quant.cuh with its rounded division taken only near a half.  With
-// r = 1 / s rounded, |d r - d / s| <= 1.6e-6 d / s < 3.2e-5 for codes up to 16 (beyond, both
-// clamp), and the rounded quotient is within 2^-20 of d / s, so away from a half by 1e-4 all of
-// them round to the same code.  Rounding is an addition of 1.5 2^23 (conversions are issued at a
-// quarter of its rate): the sum's low bits are the code.  NaN, which an infinity gives, clamps
-// to 0 as there.
-__device__ __forceinline__ uint32_t quant_word(uint4 x, const float2* sz, const float* rcp) {
+// Eight codes by quant() of quant.cuh; one copy of the code, for the rare call below.
+__device__ __noinline__ uint32_t quant_word_exact(uint4 x, uint4 sz0, uint4 sz1) {
+  const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, sz[8] = {sz0.x, sz0.y, sz0.z, sz0.w, sz1.x, sz1.y, sz1.z, sz1.w};
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float2 f = unpack_sz(sz[e]);
+    w |= quant(e & 1 ? bf16_hi(xs[e >> 1]) : bf16_lo(xs[e >> 1]), f.x, f.y) << (4 * e);
+  }
+  return w;
+}
+
+// The same with the rounded division taken only near a half.  With r = 1 / s to 2^-23,
+// |d r - d / s| <= 2.9e-6 for codes up to 16 (beyond, both clamp), and the rounded quotient is
+// within 2^-20 of d / s, so away from a half by 1e-4 all of them round to the same code.
+// Rounding is an addition of 1.5 2^23 (conversions are issued at a quarter of its rate): the
+// sum's low bits are the code.  NaN, which an infinity gives, clamps to 0 as there.
+__device__ __forceinline__ uint32_t quant_word(uint4 x, const float2* sz, const float* rcp, uint4 sz0, uint4 sz1) {
   constexpr float kMagic = 12582912.f;
   float f[8], worst = 0.f;
   bf16x8(x, f);
@@ -52,18 +63,18 @@ __device__ __forceinline__ uint32_t quant_word(uint4 x, const float2* sz, const 
     worst = fmaxf(worst, fabsf(__fsub_rn(t, __fsub_rn(up, kMagic))));
     w = (w << 4) + (__float_as_uint(up) & 15u);
   }
-  if (worst >= 0.4999f) {
-    w = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w |= quant(f[e], sz[e].x, sz[e].y) << (4 * e);
-  }
+  if (worst >= 0.4999f) w = quant_word_exact(x, sz0, sz1);
   return w;
 }
 
-// 1 / s, and 0 for s = 0 (whose code is 0).
-__device__ __forceinline__ float rcp_scale(float s) { return s == 0.f ? 0.f : __frcp_rn(s); }
+// 1 / s to 2^-23, and 0 for s = 0 (whose code is 0); binary16 scales are at least 2^-24.
+__device__ __forceinline__ float rcp_scale(float s) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return s == 0.f ? 0.f : r;
+}
 
-__global__ void __launch_bounds__(kAT, 4) append_kernel(PagedAppendArgs a) {
+__global__ void __launch_bounds__(kAT, 3) append_kernel(PagedAppendArgs a) {
   extern __shared__ int32_t prefix[];
   __shared__ AppendSmem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -173,7 +184,7 @@ __global__ void __launch_bounds__(kAT, 4) append_kernel(PagedAppendArgs a) {
         for (int e = 0; e < 8; ++e) rcp[e] = rcp_scale(sz[e].x);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint32_t*>(rec + (r0 + 16 * i) * 128 + 4 * chunk) = quant_word(k4[i], sz, rcp);
+          *reinterpret_cast<uint32_t*>(rec + (r0 + 16 * i) * 128 + 4 * chunk) = quant_word(k4[i], sz, rcp, s0, s1);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -187,12 +198,14 @@ __global__ void __launch_bounds__(kAT, 4) append_kernel(PagedAppendArgs a) {
         __half hs, hz;
         group_sz(fminf(bf16_lo(lo), bf16_hi(lo)), fmaxf(bf16_lo(hi), bf16_hi(hi)), hs, hz);
         const int row = r0 + 16 * i;
+        const uint32_t both = pack_sz(hs, hz);
         if ((chunk & 7) == 0)
-          reinterpret_cast<uint32_t*>(rec + kRecVsz)[2 * row + (chunk >> 3)] = pack_sz(hs, hz);
+          reinterpret_cast<uint32_t*>(rec + kRecVsz)[2 * row + (chunk >> 3)] = both;
         const float sv = __half2float(hs), zv = __half2float(hz), rv = rcp_scale(sv);
         const float2 sz[8] = {{sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}};
         const float rcp[8] = {rv, rv, rv, rv, rv, rv, rv, rv};
-        *reinterpret_cast<uint32_t*>(rec + row * 128 + 64 + 4 * chunk) = quant_word(v4[i], sz, rcp);
+        *reinterpret_cast<uint32_t*>(rec + row * 128 + 64 + 4 * chunk) =
+            quant_word(v4[i], sz, rcp, make_uint4(both, both, both, both), make_uint4(both, both, both, both));
       }
     }
     __syncthreads();  // every old tail row is in registers (and sm is free again)
@@ -309,7 +322,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
   if (sms <= 0) return cudaErrorInvalidDevice;
   // at most one item per entry and one more per 64 tokens
   const int64_t items = ((int64_t)a.batch + a.n_tokens / FL_PAGE) * a.p.kv_heads;
-  const int grid = (int)(items < 4 * sms ? items : 4 * sms);
+  const int grid = (int)(items < 3 * sms ? items : 3 * sms);
   return launch_pdl(append_kernel, dim3(grid), dim3(kAT), (size_t)(a.batch + 1) * 4, s, a);
 }
 
