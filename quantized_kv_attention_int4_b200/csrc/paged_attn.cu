@@ -664,6 +664,9 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       prefetch_map(&map_v);
     }
   }
+  // (launched while its predecessor ends: nothing is read or written before this)
+  grid_dep_launch();
+  grid_dep_wait();
   // the line of units, then this CTA's and this warp's stretch of it
   auto length_of = [&](int b, bool tell) {  // -1: padded
     const int s = a.slots ? __ldg(a.slots + b) : b;
@@ -1010,8 +1013,7 @@ cudaError_t launch(const PagedAttnArgs& a, int ctas, cudaStream_t s) {
   if (!rows_map(&rec, a.p.rec, (uint64_t)a.x.pages * a.p.kv_heads * (kRec / 128), kRec / 128) ||
       !rows_map(&tk, a.p.tail_k, tail_rows, 2 * kTailUnit) || !rows_map(&tv, a.p.tail_v, tail_rows, 2 * kTailUnit))
     return cudaErrorInvalidValue;
-  paged_attn_kernel<kTiles, kSel><<<ctas, Sh::kThreads, Sh::kSmem, s>>>(a, rec, tk, tv);
-  return cudaGetLastError();
+  return launch_pdl(paged_attn_kernel<kTiles, kSel>, dim3(ctas), dim3(Sh::kThreads), Sh::kSmem, s, a, rec, tk, tv);
 }
 
 template <int kTiles, bool kSel>

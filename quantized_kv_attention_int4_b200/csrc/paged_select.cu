@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
   // per product pair (m, t / 2) and lane: 2^500 q, and 2^500 15 max(q, 0), of channels t, t + 1
   __shared__ double2 s_q[2][16][32];
   grid_dep_launch();
+  grid_dep_wait();
   const int tid = threadIdx.x, lane = tid & 31, i = lane >> 2, j = lane & 3, heads = a.p.kv_heads;
   const fl_paged_index& x = a.x;
   const bool tell = blockIdx.x == 0;
@@ -299,10 +300,10 @@ __device__ __forceinline__ void topk(const unsigned long long* key, int n, int k
 __global__ void __launch_bounds__(kTT) topk_kernel(PagedAttnArgs a) {
   const int h = blockIdx.x, b = blockIdx.y, heads = a.p.kv_heads, k = a.keep;
   const fl_paged_index& x = a.x;
-  // (lengths and slots were there before the scores' launch)
+  grid_dep_launch();
+  grid_dep_wait();
   const int s = paged_slot(x, a.slots, b, false);
   const int n = s < 0 ? 0 : paged_full(paged_length(x, s, b, false));
-  grid_dep_wait();
   if (s < 0) return;
   int32_t* sel = a.sel + ((size_t)b * heads + h) * k;
   if (n <= k) {
@@ -328,11 +329,10 @@ cudaError_t launch_paged_select(const PagedAttnArgs& a, cudaStream_t s) {
   if (scored) {
     const int64_t items = (int64_t)a.batch * ((a.x.max_pages + kChunk - 1) / kChunk) * a.p.kv_heads;
     const int grid = (int)(items < 2 * sms ? items : 2 * sms);
-    score_kernel<<<grid, kST, (size_t)(a.batch + 1) * 4, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_pdl(score_kernel, dim3(grid), dim3(kST), (size_t)(a.batch + 1) * 4, s, a);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl_if(scored, topk_kernel, dim3(a.p.kv_heads, a.batch), dim3(kTT), 0, s, a);
+  return launch_pdl(topk_kernel, dim3(a.p.kv_heads, a.batch), dim3(kTT), 0, s, a);
 }
 
 }  // namespace fl
