@@ -11,9 +11,10 @@
 //                 instruction, which the SM issues at a quarter of this rate): the exponent
 //                 keeps its bias, which scales the number by 2^-1008, subnormals included;
 //                 the queries carry 2^500 of that and the sum the rest.
-//   topk_kernel   one CTA per (entry, head): radix select on the scores' 64-bit images
-//                 from the highest bit in which they differ, the keys of up to 2048 blocks
-//                 held in registers, then the chosen blocks in order.
+//   topk          on the scores' 64-bit images, from the highest bit in which they differ:
+//                 up to 256 blocks a warp per (entry, head) with every key in registers and
+//                 one count a bit, until exactly k keys are left above; beyond, one CTA per
+//                 (entry, head) and a radix select, ten bits a pass.
 #include "paged.cuh"
 
 namespace fl {
@@ -22,7 +23,6 @@ namespace {
 constexpr int kST = 256;   // threads of the score kernel: 8 blocks a warp
 constexpr int kChunk = 64; // blocks it takes at a time
 constexpr int kTT = 256;   // threads of the top-k kernel
-constexpr int kHeld = 8;   // keys a thread of it holds
 constexpr int kDigit = 10;
 
 __device__ __forceinline__ unsigned long long score_image(double v) {
@@ -38,8 +38,9 @@ __device__ __forceinline__ void mma_f64(double (&c)[2], double a, double b) {
 
 // Eight queries of a group at a time (its last one is repeated to fill them).  A CTA takes an
 // equal, consecutive share of the chunks of 64 blocks, so that it stages the queries of an
-// (entry, head) once; while it computes on a chunk, the records of the next one and the page
-// numbers of the one after are on their way.  Lane (i, j) reads channels 16 m + 4 j + t of
+// (entry, head) once.  A record's words are replaced by the next chunk's as the products use them
+// up, and the page numbers of the chunk after that are on their way: loads issued in one go kept
+// the warps from computing until the memory system had taken them all.  Lane (i, j) reads channels 16 m + 4 j + t of
 // block i, and these are the columns of product (m, t).
 __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
   extern __shared__ int32_t prefix[];
@@ -87,11 +88,7 @@ __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
     if (j == 0) paged_error(x, FL_DEV_PAGE_RANGE, p.b);
     return -1;
   };
-  auto scales = [&](const At& p, int page, uint4 (&sz)[8]) {
-    const uint8_t* rec = a.p.rec + ((size_t)max(page, 0) * heads + p.h) * kRec + kRecKsz + 16 * j;
-#pragma unroll
-    for (int m = 0; m < 8; ++m) sz[m] = ldg_u4(rec + 64 * m);
-  };
+  auto scales = [&](const At& p, int page) { return a.p.rec + ((size_t)max(page, 0) * heads + p.h) * kRec + kRecKsz + 16 * j; };
   At cur, ahead;
   enter(cur, paged_find(prefix, a.batch, w));
   cur.h = (w - prefix[cur.b]) / cur.chunks;
@@ -102,25 +99,22 @@ __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
     next(ahead);  // ahead is the chunk behind the current one
     page1 = page_of(ahead);
   }
-  uint4 sz[8], sz1[8];
-  scales(cur, page, sz);
+  uint4 sz[8];
+#pragma unroll
+  for (int m = 0; m < 8; ++m) sz[m] = ldg_u4(scales(cur, page) + 64 * m);
   int staged_b = -1, staged_h = -1;
   for (; w < end; ++w) {
     At after = ahead;
     int page2 = -1;
-    if (w + 1 < end) scales(ahead, page1, sz1);
+    const uint8_t* rec1 = w + 1 < end ? scales(ahead, page1) : nullptr;
     if (w + 2 < end) {
       next(after);
       page2 = page_of(after);
     }
     // infinite or NaN scales and zeros (exponent 31) carry into the halves' top bits; such a
     // block, or one that cannot be read, ranks last
-    uint32_t over = 0;
-#pragma unroll
-    for (int m = 0; m < 8; ++m)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) over |= ((&sz[m].x)[c] & 0x7fff7fffu) + 0x04000400u;
-    bool nan = page < 0 || (over & 0x80008000u);
+    uint32_t over = page < 0 ? 0x80008000u : 0u;
+    bool nan = false;
     double best = -INFINITY;
     for (int g0 = 0; g0 < a.group; g0 += 8) {
       if (a.group > 8 || cur.b != staged_b || cur.h != staged_h) {
@@ -137,7 +131,7 @@ __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
         staged_h = cur.h;
         __syncthreads();
       }
-      double sum[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
+      double sum[4][2] = {};  // four chains of 16 products
 #pragma unroll
       for (int m = 0; m < 8; ++m)
 #pragma unroll
@@ -147,13 +141,15 @@ __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
           for (int y = 0; y < 2; ++y) {
             uint32_t v = (&sz[m].x)[t + y];
             asm volatile("" : "+r"(v));  // widened here each time: 128 registers more if hoisted out of the loop
-            mma_f64(sum[0], __hiloint2double((int)(((v >> 6) & 0x01fffc00u) | (v & 0x80000000u)), 0), y ? q.y : q.x);
-            mma_f64(sum[1], __hiloint2double((int)((v & 0x7fffu) << 10), 0), y ? p.y : p.x);
+            mma_f64(sum[2 * y], __hiloint2double((int)(((v >> 6) & 0x01fffc00u) | (v & 0x80000000u)), 0), y ? q.y : q.x);
+            mma_f64(sum[2 * y + 1], __hiloint2double((int)((v & 0x7fffu) << 10), 0), y ? p.y : p.x);
+            over |= (v & 0x7fff7fffu) + 0x04000400u;
           }
+          if (t == 2 && rec1 && g0 + 8 >= a.group) sz[m] = ldg_u4(rec1 + 64 * m);
         }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const double v = (sum[0][y] + sum[1][y]) * 0x1p508;
+        const double v = ((sum[0][y] + sum[1][y]) + (sum[2][y] + sum[3][y])) * 0x1p508;
         nan |= v != v;
         best = fmax(best, v);
       }
@@ -161,7 +157,7 @@ __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
     // the block's best over the four lanes of its queries
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) best = fmax(best, __shfl_xor_sync(kFull, best, o));
-    const bool bad = (__ballot_sync(kFull, nan) >> (4 * i)) & 15u;
+    const bool bad = (__ballot_sync(kFull, nan || (over & 0x80008000u)) >> (4 * i)) & 15u;
     const int block = cur.c * kChunk + (tid >> 2);
     if (j == 0 && block < cur.full)
       (static_cast<unsigned long long*>(a.data) + ((size_t)cur.b * heads + cur.h) * x.max_pages)[block] = bad ? 0ull : score_image(best);
@@ -169,37 +165,112 @@ __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
     ahead = after;
     page = page1;
     page1 = page2;
-#pragma unroll
-    for (int m = 0; m < 8; ++m) sz[m] = sz1[m];
   }
 }
 
-// The k-th largest of n > k keys and the blocks to take; kSmall: n <= kHeld kTT, keys in
-// registers.
-template <bool kSmall>
-__device__ __forceinline__ void topk(const unsigned long long* key, int n, int k, int32_t* sel) {
+constexpr int kWarpKeys = 8;
+
+// A warp per (entry, head) with at most 32 kWarpKeys blocks: lane l holds keys 32 y + l.
+__global__ void __launch_bounds__(128) topk_warp_kernel(PagedAttnArgs a) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, heads = a.p.kv_heads, k = a.keep;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= (int64_t)a.batch * heads) return;
+  const int b = (int)(row / heads);
+  const fl_paged_index& x = a.x;
+  const int s = paged_slot(x, a.slots, b, false);
+  if (s < 0) return;
+  const int n = paged_full(paged_length(x, s, b, false));
+  int32_t* sel = a.sel + row * k;
+  if (n <= k) {
+    for (int i = lane; i < k; i += 32) sel[i] = i < n ? i : -1;
+    return;
+  }
+  const unsigned long long* from = static_cast<const unsigned long long*>(a.data) + row * x.max_pages;
+  unsigned long long key[kWarpKeys];
+  unsigned long long lo = ~0ull, hi = 0ull;
+#pragma unroll
+  for (int y = 0; y < kWarpKeys; ++y) {
+    const int i = 32 * y + lane;
+    key[y] = i < n ? __ldcg(from + i) : 0ull;
+  }
+#pragma unroll
+  for (int y = 0; y < kWarpKeys; ++y) {
+    lo = 32 * y + lane < n ? min(lo, key[y]) : lo;
+    hi = max(hi, key[y]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = min(lo, __shfl_xor_sync(kFull, lo, o));
+    hi = max(hi, __shfl_xor_sync(kFull, hi, o));
+  }
+  // `floor`: the largest number so far that at least k keys reach (entries behind the last key
+  // are 0, below every floor > lo); bit by bit
+  int bit = lo == hi ? -1 : 63 - __clzll((long long)(lo ^ hi));
+  unsigned long long floor = bit < 0 ? lo : bit == 63 ? 0ull : hi & (~0ull << (bit + 1));
+  int reach = n;
+  for (; bit >= 0 && reach != k; --bit) {
+    const unsigned long long t = floor | 1ull << bit;
+    int c = 0;
+#pragma unroll
+    for (int y = 0; y < kWarpKeys; ++y) c += key[y] >= t;
+    c = __reduce_add_sync(kFull, c);
+    if (c >= k) {
+      floor = t;
+      reach = c;
+    }
+  }
+  // exactly k reach it; or, where keys are equal, the first of those
+  int above = 0;
+  if (reach != k) {
+    int c = 0;
+#pragma unroll
+    for (int y = 0; y < kWarpKeys; ++y) c += key[y] > floor;
+    above = __reduce_add_sync(kFull, c);
+  }
+  int equal = reach != k ? k - above : 0, at = 0;  // how many of the keys equal to it to take
+#pragma unroll
+  for (int y = 0; y < kWarpKeys; ++y) {
+    if (32 * y >= n) break;
+    const bool in = 32 * y + lane < n;
+    bool take = in && (reach == k ? key[y] >= floor : key[y] > floor);
+    if (reach != k) {
+      const unsigned eq = __ballot_sync(kFull, in && key[y] == floor);
+      take |= (eq >> lane & 1u) && __popc(eq & ((1u << lane) - 1u)) < equal;
+      equal -= min(equal, __popc(eq));
+    }
+    const unsigned taken = __ballot_sync(kFull, take);
+    if (take) sel[at + __popc(taken & ((1u << lane) - 1u))] = 32 * y + lane;
+    at += __popc(taken);
+  }
+}
+
+// A CTA per (entry, head): the k-th largest of n > k keys digit by digit.
+__global__ void __launch_bounds__(kTT) topk_kernel(PagedAttnArgs a) {
   __shared__ unsigned hist[1 << kDigit];
   __shared__ unsigned long long s_lo[kTT / 32], s_hi[kTT / 32];
   __shared__ int red[kTT / 32];
   __shared__ int s_digit, s_above, s_count;
+  const int h = blockIdx.x, b = blockIdx.y, heads = a.p.kv_heads, k = a.keep;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // thread t holds keys kHeld t .. + kHeld - 1, so that block order is thread order
-  unsigned long long held[kHeld];
+  const fl_paged_index& x = a.x;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int s = paged_slot(x, a.slots, b, false);
+  if (s < 0) return;
+  const int n = paged_full(paged_length(x, s, b, false));
+  int32_t* sel = a.sel + ((size_t)b * heads + h) * k;
+  if (n <= k) {
+    for (int i = tid; i < k; i += kTT) sel[i] = i < n ? i : -1;
+    return;
+  }
+  const unsigned long long* key = static_cast<const unsigned long long*>(a.data) + ((size_t)b * heads + h) * x.max_pages;
   unsigned long long lo = ~0ull, hi = 0ull;
-  if constexpr (kSmall) {
-#pragma unroll
-    for (int y = 0; y < kHeld; ++y) {
-      const int i = kHeld * tid + y;
-      held[y] = i < n ? __ldcg(key + i) : 0ull;
-      lo = i < n ? min(lo, held[y]) : lo;
-      hi = max(hi, held[y]);
-    }
-  } else {
-    for (int i = tid; i < n; i += kTT) {
-      const unsigned long long u = __ldcg(key + i);
-      lo = min(lo, u);
-      hi = max(hi, u);
-    }
+  for (int i = tid; i < n; i += kTT) {
+    const unsigned long long u = __ldcg(key + i);
+    lo = min(lo, u);
+    hi = max(hi, u);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -227,15 +298,9 @@ __device__ __forceinline__ void topk(const unsigned long long* key, int n, int k
     shift -= wb;
     const int nb = 1 << wb;
     const unsigned dmask = (unsigned)nb - 1u;
-    if constexpr (kSmall) {
-#pragma unroll
-      for (int y = 0; y < kHeld; ++y)
-        if (kHeld * tid + y < n && (held[y] & known) == prefix) atomicAdd(&hist[(unsigned)(held[y] >> shift) & dmask], 1u);
-    } else {
-      for (int i = tid; i < n; i += kTT) {
-        const unsigned long long u = __ldcg(key + i);
-        if ((u & known) == prefix) atomicAdd(&hist[(unsigned)(u >> shift) & dmask], 1u);
-      }
+    for (int i = tid; i < n; i += kTT) {
+      const unsigned long long u = __ldcg(key + i);
+      if ((u & known) == prefix) atomicAdd(&hist[(unsigned)(u >> shift) & dmask], 1u);
     }
     __syncthreads();
     constexpr int kPer = (1 << kDigit) / kTT;
@@ -269,50 +334,17 @@ __device__ __forceinline__ void topk(const unsigned long long* key, int n, int k
   }
   // every key above the wanted one, and the first krem equal to it, in block order
   int gt_run = 0, eq_run = 0;
-  constexpr int kStep = kSmall ? kHeld * kTT : kTT, kMine = kSmall ? kHeld : 1;
-  for (int i0 = 0; i0 < n; i0 += kStep) {
-    unsigned gts = 0, eqs = 0;
-#pragma unroll
-    for (int y = 0; y < kMine; ++y) {
-      const int i = i0 + kMine * tid + y;
-      if (i < n) {
-        const unsigned long long m = (kSmall ? held[y] : __ldcg(key + i)) & known;
-        gts |= m > prefix ? 1u << y : 0u;
-        eqs |= m == prefix ? 1u << y : 0u;
-      }
-    }
+  for (int i0 = 0; i0 < n; i0 += kTT) {
+    const int i = i0 + tid;
+    const unsigned long long m = i < n ? __ldcg(key + i) & known : 0ull;
+    const bool gt = i < n && m > prefix, eq = i < n && m == prefix;
     int total;
-    const int before = paged_block_scan<kTT>(__popc(gts) << 16 | __popc(eqs), red, total);
-    int g = gt_run + (before >> 16), e = eq_run + (before & 0xffff);
-#pragma unroll
-    for (int y = 0; y < kMine; ++y) {
-      if ((gts >> y) & 1u) sel[g++ + min(e, krem)] = i0 + kMine * tid + y;
-      if ((eqs >> y) & 1u) {
-        if (e < krem) sel[g + e] = i0 + kMine * tid + y;
-        ++e;
-      }
-    }
+    const int before = paged_block_scan<kTT>((gt ? 1 << 16 : 0) | (eq ? 1 : 0), red, total);
+    const int g = gt_run + (before >> 16), e = eq_run + (before & 0xffff);
+    if (gt || (eq && e < krem)) sel[g + min(e, krem)] = i;
     gt_run += total >> 16;
     eq_run += total & 0xffff;
   }
-}
-
-__global__ void __launch_bounds__(kTT) topk_kernel(PagedAttnArgs a) {
-  const int h = blockIdx.x, b = blockIdx.y, heads = a.p.kv_heads, k = a.keep;
-  const fl_paged_index& x = a.x;
-  grid_dep_launch();
-  grid_dep_wait();
-  const int s = paged_slot(x, a.slots, b, false);
-  const int n = s < 0 ? 0 : paged_full(paged_length(x, s, b, false));
-  if (s < 0) return;
-  int32_t* sel = a.sel + ((size_t)b * heads + h) * k;
-  if (n <= k) {
-    for (int i = threadIdx.x; i < k; i += kTT) sel[i] = i < n ? i : -1;
-    return;
-  }
-  const unsigned long long* key = static_cast<const unsigned long long*>(a.data) + ((size_t)b * heads + h) * x.max_pages;
-  if (n <= kHeld * kTT) topk<true>(key, n, k, sel);
-  else topk<false>(key, n, k, sel);
 }
 
 }  // namespace
@@ -332,6 +364,11 @@ cudaError_t launch_paged_select(const PagedAttnArgs& a, cudaStream_t s) {
     const cudaError_t e = launch_pdl(score_kernel, dim3(grid), dim3(kST), (size_t)(a.batch + 1) * 4, s, a);
     if (e != cudaSuccess) return e;
   }
+  // What a request can have decides, not what it has: lengths are the device's.  By kernel time:
+  // up to 256 blocks a warp 5.7 us, the CTA 7.4; 511 blocks a warp (16 keys a lane) 7.9, the CTA 7.0.
+  const int most = a.x.max_pages - 1;
+  const unsigned grid = (unsigned)(((int64_t)a.batch * a.p.kv_heads + 3) / 4);
+  if (most <= 32 * kWarpKeys || !scored) return launch_pdl(topk_warp_kernel, dim3(grid), dim3(128), 0, s, a);
   return launch_pdl(topk_kernel, dim3(a.p.kv_heads, a.batch), dim3(kTT), 0, s, a);
 }
 
