@@ -150,10 +150,12 @@ struct Segment {
   int begin, end, b, h, ch;
 };
 
-template <int kHeads, bool kSel>
+// kOne: a group's query heads make one segment (chunks = 1).
+template <int kHeads, bool kSel, bool kOne>
 struct Line {
   const PagedAttnArgs& a;
-  int chunks;
+
+  __device__ __forceinline__ int chunks() const { return kOne ? 1 : (a.group + kHeads - 1) / kHeads; }
 
   __device__ __forceinline__ int blocks_of(int n) const {
     const int full = paged_full(n);
@@ -172,8 +174,10 @@ struct Line {
   __device__ __forceinline__ void next(Cursor& c) const {
     if (++c.u < c.units) return;
     c.u = 0;
-    if (++c.ch < chunks) return;
-    c.ch = 0;
+    if (!kOne) {
+      if (++c.ch < chunks()) return;
+      c.ch = 0;
+    }
     if (++c.h < a.p.kv_heads) return;
     c.h = 0;
 #pragma unroll 1
@@ -185,17 +189,17 @@ struct Line {
     }
   }
   // The first query head, and how many
-  __device__ __forceinline__ int head(int h, int ch) const { return h * a.group + ch * kHeads; }
-  __device__ __forceinline__ int live(int ch) const { return min(kHeads, a.group - ch * kHeads); }
+  __device__ __forceinline__ int head(int h, int ch) const { return h * a.group + (kOne ? 0 : ch * kHeads); }
+  __device__ __forceinline__ int live(int ch) const { return kOne ? a.group : min(kHeads, a.group - ch * kHeads); }
 };
 
-// Errors of one lane, told at the kernel's end (one place of the code): the first one's code and
-// entry, and how many.
+// Errors of a CTA, told at its end: the first one's code and entry, and how many.  In shared
+// memory: they are rare, and registers are not.
 struct Errors {
-  int first = 0, detail = 0, count = 0;
+  int first, detail, count;
 
   __device__ __forceinline__ void add(int code, int b) {
-    if (count++ == 0) {
+    if (atomicAdd(&count, 1) == 0) {
       first = code;
       detail = b;
     }
@@ -636,7 +640,7 @@ __device__ __forceinline__ void join(int n, F&& part, float4& o, float& m, float
   }
 }
 
-template <int kTiles, bool kSel>
+template <int kTiles, bool kSel, bool kOne>
 __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     paged_attn_kernel(const PagedAttnArgs a, const __grid_constant__ CUtensorMap map_rec,
                       const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
@@ -646,19 +650,21 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
   __shared__ int red[Sh::kWarps];
   __shared__ Segment s_own[Sh::kWarps][2];  // segments whose first piece in this CTA a warp holds
   __shared__ int s_owned[Sh::kWarps];
+  __shared__ Errors errors;
   __shared__ int s_begin[Sh::kWarps + 1];       // the warps' stretches
   __shared__ int s_total, s_ctas;
   __shared__ const float* s_first[Sh::kWarps];  // where the state of a warp's first piece is
   uint8_t* stages = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int heads = a.p.kv_heads, chunks = (a.group + Sh::kHeads - 1) / Sh::kHeads;
-  const Line<Sh::kHeads, kSel> line{a, chunks};
-  Errors errors;
+  const int heads = a.p.kv_heads;
+  const Line<Sh::kHeads, kSel, kOne> line{a};
 
   if (lane == 0) {
     for (int d = 0; d < Sh::kDepth; ++d) mbar_init(&bars[warp][d], 1);
     fence_mbar_init();
+    s_owned[warp] = 0;
     if (warp == 0) {
+      errors.count = 0;
       prefetch_map(&map_rec);
       prefetch_map(&map_k);
       prefetch_map(&map_v);
@@ -667,6 +673,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
   // (launched while its predecessor ends: nothing is read or written before this)
   grid_dep_launch();
   grid_dep_wait();
+  __syncthreads();
   // the line of units, then this CTA's and this warp's stretch of it
   auto length_of = [&](int b, bool tell) {  // -1: padded
     const int s = a.slots ? __ldg(a.slots + b) : b;
@@ -679,7 +686,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     if (tell) errors.add(FL_DEV_TOO_LONG, b);
     return 0;
   };
-  const int per_entry = heads * chunks;  // segments of an entry
+  const int per_entry = heads * line.chunks();  // segments of an entry
   int total = 0, most = 0, segments = 0;  // units, units of the longest segment
   int clo, chi, wlo, whi;
   // A small call takes fewer CTAs (a warp should have a unit).  One whose segments have all the
@@ -758,8 +765,9 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     __syncthreads();  // the stages take over from the prefix sums
     fence_proxy_async();
   }
-  if (clo == chi) {
-    errors.tell(a.x);
+  if (clo == chi) {  // (CTA 0, which looks at the entries, has units or there are none)
+    __syncthreads();
+    if (threadIdx.x == 0) errors.tell(a.x);
     return;
   }
   if (wlo < whi) {
@@ -767,8 +775,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     line.place(use, use.n);
     const int seg = left / use.units;
     use.u = left - seg * use.units;
-    use.h = chunks == 1 ? seg : seg / chunks;
-    use.ch = seg - use.h * chunks;
+    use.h = kOne ? seg : seg / line.chunks();
+    use.ch = seg - use.h * line.chunks();
   }
 
   // states of pieces: the last one of a warp in its own stages, one before it in the workspace
@@ -777,7 +785,6 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     return static_cast<float*>(a.data) + (size_t)(blockIdx.x * Sh::kWarps + w) * Sh::kHeads * kPart;
   };
 
-  int n_own = 0;
   if (wlo < whi) {
     Query<kTiles> qr;
     State<kTiles> s;
@@ -876,10 +883,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
         }
         if (pos - piece == wlo && lane == 0) s_first[warp] = part;
         // the first piece of a segment in this CTA joins the others
-        if (!whole && pos - piece == max(seg.begin, s_begin[0])) {
-          if (lane == 0) s_own[warp][n_own] = seg;
-          ++n_own;
-        }
+        if (!whole && pos - piece == max(seg.begin, s_begin[0]) && lane == 0) s_own[warp][s_owned[warp]++] = seg;
       }
       if (!more) break;
       seg = Segment{pos - use.u, pos - use.u + use.units, use.b, use.h, use.ch};
@@ -919,9 +923,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       line.next(use);
     }
   }
-  if (lane == 0) s_owned[warp] = n_own;
-  errors.tell(a.x);
   __syncthreads();
+  if (threadIdx.x == 0) errors.tell(a.x);
 
   // head g of the segments that warp w holds is joined by warp w + g.  (The stretches are read
   // again: kept in registers over the loop above they would be spilled.)
@@ -1005,20 +1008,29 @@ bool rows_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box) {
 std::atomic<bool> g_attr_done[kMaxDevices];
 std::mutex g_attr_mu;
 
-template <int kTiles, bool kSel>
-cudaError_t launch(const PagedAttnArgs& a, int ctas, cudaStream_t s) {
+template <int kTiles, bool kSel, bool kOne>
+cudaError_t launch_as(const PagedAttnArgs& a, int ctas, cudaStream_t s) {
   using Sh = Shape<kTiles>;
   CUtensorMap rec, tk, tv;
   const uint64_t tail_rows = (uint64_t)a.x.slots * a.p.kv_heads * 2 * FL_PAGE;
   if (!rows_map(&rec, a.p.rec, (uint64_t)a.x.pages * a.p.kv_heads * (kRec / 128), kRec / 128) ||
       !rows_map(&tk, a.p.tail_k, tail_rows, 2 * kTailUnit) || !rows_map(&tv, a.p.tail_v, tail_rows, 2 * kTailUnit))
     return cudaErrorInvalidValue;
-  return launch_pdl(paged_attn_kernel<kTiles, kSel>, dim3(ctas), dim3(Sh::kThreads), Sh::kSmem, s, a, rec, tk, tv);
+  return launch_pdl(paged_attn_kernel<kTiles, kSel, kOne>, dim3(ctas), dim3(Sh::kThreads), Sh::kSmem, s, a, rec, tk, tv);
 }
 
-template <int kTiles, bool kSel>
+template <int kTiles, bool kSel, bool kOne>
 cudaError_t allow_smem() {
-  return cudaFuncSetAttribute(paged_attn_kernel<kTiles, kSel>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<kTiles>::kSmem);
+  return cudaFuncSetAttribute(paged_attn_kernel<kTiles, kSel, kOne>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Shape<kTiles>::kSmem);
+}
+
+// Up to 4 query heads a group one tile of 8 columns, up to 8 two; beyond, several segments.
+template <bool kSel>
+cudaError_t launch(const PagedAttnArgs& a, int ctas, cudaStream_t s) {
+  if (a.group <= 4) return launch_as<1, kSel, true>(a, ctas, s);
+  if (a.group <= 8) return launch_as<2, kSel, true>(a, ctas, s);
+  return launch_as<2, kSel, false>(a, ctas, s);
 }
 
 }  // namespace
@@ -1033,16 +1045,17 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
   const cudaError_t e = once_per_device(g_attr_done, g_attr_mu, [](int) {
-    cudaError_t r = allow_smem<1, false>();
-    if (r == cudaSuccess) r = allow_smem<1, true>();
-    if (r == cudaSuccess) r = allow_smem<2, false>();
-    if (r == cudaSuccess) r = allow_smem<2, true>();
+    cudaError_t r = allow_smem<1, false, true>();
+    if (r == cudaSuccess) r = allow_smem<1, true, true>();
+    if (r == cudaSuccess) r = allow_smem<2, false, true>();
+    if (r == cudaSuccess) r = allow_smem<2, true, true>();
+    if (r == cudaSuccess) r = allow_smem<2, false, false>();
+    if (r == cudaSuccess) r = allow_smem<2, true, false>();
     return r;
   });
   if (e != cudaSuccess) return e;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  if (a.group <= 4) return a.sel ? launch<1, true>(a, ctas, s) : launch<1, false>(a, ctas, s);
-  return a.sel ? launch<2, true>(a, ctas, s) : launch<2, false>(a, ctas, s);
+  return a.sel ? launch<true>(a, ctas, s) : launch<false>(a, ctas, s);
 }
 
 }  // namespace fl
