@@ -52,8 +52,8 @@ uint64_t data_bytes(const fl_paged_index& x, const fl_paged_pool& p, int batch, 
 fl_status check_heads(const fl_paged_index* x, const fl_paged_pool* p, int32_t batch, int32_t q_heads) {
   if (q_heads < 1 || q_heads % p->kv_heads) return FL_ERR_INVALID;
   // work units of one call are counted in 32 bits: blocks and quarters of a tail, per entry,
-  // key-value head and eight query heads
-  const int64_t chunks = (q_heads / p->kv_heads + 7) / 8;
+  // key-value head and four query heads
+  const int64_t chunks = (q_heads / p->kv_heads + 3) / 4;
   if ((int64_t)batch * p->kv_heads * chunks * ((int64_t)x->max_pages + 4) > INT32_MAX) return FL_ERR_UNSUPPORTED;
   return FL_OK;
 }

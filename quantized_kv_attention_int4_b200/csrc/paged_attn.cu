@@ -847,7 +847,8 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
 #pragma unroll 1
     for (;;) {
       const bool more = k < count;
-      if (more) qr.fetch(a, use.b, line.head(use.h, use.ch), line.live(use.ch));
+      // (with two tiles the registers do not allow it)
+      if (kTiles == 1 && more) qr.fetch(a, use.b, line.head(use.h, use.ch), line.live(use.ch));
       if (k > 0) {
         // this lane's channels of head j: 32 q + 4 i .. + 3
         const int i = lane >> 2, j = lane & 3;
@@ -892,6 +893,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
       const int tail_rows = use.n - FL_PAGE * paged_full(use.n);
 #pragma unroll 1
       while (issued < count && issued < k + Sh::kDepth) issue();  // (the first turn)
+      if (kTiles > 1) qr.fetch(a, use.b, line.head(use.h, use.ch), line.live(use.ch));
       qr.prepare();
 #pragma unroll 1
       for (int x = 0; x < piece; ++x, ++k) {
@@ -1025,10 +1027,18 @@ cudaError_t allow_smem() {
                               Shape<kTiles>::kSmem);
 }
 
-// Up to 4 query heads a group one tile of 8 columns, up to 8 two; beyond, several segments.
+// Up to 4 query heads a group make one tile of 8 columns.  More take two tiles, which halves
+// the work on the codes, where there is much of it, and two segments of one tile where there is
+// little (by what the call can hold: lengths are the device's): the larger code and its fewer
+// warps start more slowly.  4 x 8 heads, 16 x 16384: two tiles 112 us, two segments 139; 64 x
+// 8191 with 16 blocks kept: the step 33.3 and 31.2; 8 requests of up to 100: 13.1 and 8.2.
+constexpr int kFewUnits = 8;  // a warp
+
 template <bool kSel>
 cudaError_t launch(const PagedAttnArgs& a, int ctas, cudaStream_t s) {
   if (a.group <= 4) return launch_as<1, kSel, true>(a, ctas, s);
+  const int64_t units = (int64_t)a.batch * a.p.kv_heads * ((kSel && a.keep < a.x.max_pages ? a.keep : a.x.max_pages) + FL_PAGE / kTailUnit);
+  if (units <= (int64_t)kFewUnits * Shape<1>::kWarps * ctas) return launch_as<1, kSel, false>(a, ctas, s);
   if (a.group <= 8) return launch_as<2, kSel, true>(a, ctas, s);
   return launch_as<2, kSel, false>(a, ctas, s);
 }
@@ -1036,8 +1046,8 @@ cudaError_t launch(const PagedAttnArgs& a, int ctas, cudaStream_t s) {
 }  // namespace
 
 uint64_t paged_attn_bytes(const fl_paged_pool& p, int q_heads) {
-  const uint64_t heads = q_heads / p.kv_heads <= 4 ? 4 : 8, warps = heads == 4 ? Shape<1>::kWarps : Shape<2>::kWarps;
-  return (uint64_t)kMaxCtas * (warps + 2) * heads * kPart * sizeof(float);
+  const uint64_t one = (Shape<1>::kWarps + 2) * Shape<1>::kHeads, two = (Shape<2>::kWarps + 2) * Shape<2>::kHeads;
+  return (uint64_t)kMaxCtas * (q_heads / p.kv_heads <= 4 || one > two ? one : two) * kPart * sizeof(float);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
@@ -1047,6 +1057,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
   const cudaError_t e = once_per_device(g_attr_done, g_attr_mu, [](int) {
     cudaError_t r = allow_smem<1, false, true>();
     if (r == cudaSuccess) r = allow_smem<1, true, true>();
+    if (r == cudaSuccess) r = allow_smem<1, false, false>();
+    if (r == cudaSuccess) r = allow_smem<1, true, false>();
     if (r == cudaSuccess) r = allow_smem<2, false, true>();
     if (r == cudaSuccess) r = allow_smem<2, true, true>();
     if (r == cudaSuccess) r = allow_smem<2, false, false>();
