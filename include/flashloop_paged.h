@@ -36,6 +36,9 @@
  *     events), also when they are replayed from CUDA graphs: two graphs that hold calls on
  *     one workspace must not run at the same time.
  *   - Offsets into pools are computed in 64 bits.
+ *   - Every call is ordered behind the stream's earlier work as any launch is.  (The kernels are
+ *     launched programmatically: their first instructions may run while the predecessor ends,
+ *     and they wait for it before they touch memory.)
  */
 #ifndef FLASHLOOP_PAGED_H
 #define FLASHLOOP_PAGED_H
@@ -122,8 +125,8 @@ fl_status fl_paged_append(const fl_paged_index* index, const fl_paged_pool* pool
                           const uint16_t* v, int64_t token_stride, int64_t head_stride, void* stream);
 
 /* Cached tokens as BF16 rows: row t of k, v (same addressing and alignment as
- * fl_paged_append's) receives the token at place[t] (fl_paged_slot_map's): fma(code, s, z)
- * rounded to BF16, or the tail's row.  Rows with place -1 are left as they were. */
+ * fl_paged_append's, rows that do not overlap) receives the token at place[t]
+ * (fl_paged_slot_map's): fma(code, s, z) rounded to BF16, or the tail's row.  Rows with place -1 are left as they were. */
 fl_status fl_paged_read(const fl_paged_index* index, const fl_paged_pool* pool, int32_t n_tokens,
                         const int32_t* place, uint16_t* k, uint16_t* v, int64_t token_stride, int64_t head_stride,
                         void* stream);
@@ -148,12 +151,12 @@ fl_status fl_paged_select(const fl_paged_index* index, const fl_paged_pool* pool
                           int32_t keep, int32_t* sel, void* ws, size_t ws_bytes, void* stream);
 
 /* Attention of one token per request over its whole cache (sel == NULL), or over the blocks
- * sel[batch][kv_heads][keep] names (ascending, -1 behind the last; fl_paged_select's) and
+ * sel[batch][kv_heads][keep] names (each once, -1 behind the last; fl_paged_select's) and
  * the tail:  o = softmax(q K^T / sqrt(128)) V, with K, V = fma(code, s, z) or the tail's
  * rows.  q: BF16, entry i and head h at q + i q_batch_stride + h q_head_stride (16-byte
  * aligned, strides multiples of 8); query heads g kv .. of a group share key-value head
  * h = head / (q_heads / kv_heads), q_heads a multiple of kv_heads.  o: fp32, strides
- * multiples of 4, 16-byte aligned.  lse: NULL or fp32 [batch][q_heads], the base-2 logarithm
+ * multiples of 4, 16-byte aligned, rows that do not overlap.  lse: NULL or fp32 [batch][q_heads], the base-2 logarithm
  * of the sum of 2^score with scores in base 2 (q.k log2(e) / sqrt(128)).  A request of no
  * tokens gives o = 0 and lse = -inf; rows of padded entries are left as they were.  Sums in
  * fp32; results do not depend on what else is in the batch beyond fp32 rounding, and are the

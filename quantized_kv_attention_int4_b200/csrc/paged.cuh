@@ -54,6 +54,15 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s);
 uint64_t paged_select_bytes(const fl_paged_index& x, const fl_paged_pool& p, int batch);
 uint64_t paged_attn_bytes(const fl_paged_pool& p, int q_heads);
 
+// Plain loads.  These kernels start while their predecessor is still writing what they will read
+// once they have waited for it (programmatic launch), so nothing they read may go through the
+// read-only path, which wants data that no one writes while the kernel runs.
+template <class T>
+__device__ __forceinline__ T ld(const T* p) {
+  return *p;
+}
+__device__ __forceinline__ uint4 ld_u4(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+
 // Blocks of a request of n tokens that are records.
 __host__ __device__ __forceinline__ int paged_full(int n) { return n > 0 ? (n - 1) >> 6 : 0; }
 
@@ -64,7 +73,7 @@ __device__ __forceinline__ void paged_error(const fl_paged_index& x, int code, i
 // The table row of batch entry b, or -1 for a padded entry or one out of range (recorded
 // when `tell`).
 __device__ __forceinline__ int paged_slot(const fl_paged_index& x, const int32_t* slots, int b, bool tell) {
-  const int s = slots ? __ldg(slots + b) : b;
+  const int s = slots ? ld(slots + b) : b;
   if (s >= 0 && s < x.slots) return s;
   if (s != -1 && tell) paged_error(x, FL_DEV_SLOT_RANGE, b);
   return -1;

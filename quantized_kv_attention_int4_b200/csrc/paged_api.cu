@@ -44,6 +44,14 @@ fl_status check_batch(const fl_paged_index* x, int32_t batch, const int32_t* slo
 // Strides in elements of `unit`-element rows: multiples of `unit`, none negative.
 bool good_strides(int64_t a, int64_t b, int unit) { return a >= 0 && b >= 0 && a % unit == 0 && b % unit == 0; }
 
+// Whether n0 x n1 rows of 128 elements at i s0 + j s1 lie apart from one another: outputs that
+// overlap would be written by several warps at once.
+bool rows_apart(int64_t n0, int64_t s0, int64_t n1, int64_t s1) {
+  if (n0 == 1) return n1 == 1 || s1 >= FL_HEAD_DIM;
+  if (n1 == 1) return s0 >= FL_HEAD_DIM;
+  return (s1 >= FL_HEAD_DIM && s0 >= (n1 - 1) * s1 + FL_HEAD_DIM) || (s0 >= FL_HEAD_DIM && s1 >= (n0 - 1) * s0 + FL_HEAD_DIM);
+}
+
 uint64_t data_bytes(const fl_paged_index& x, const fl_paged_pool& p, int batch, int q_heads) {
   const uint64_t a = paged_select_bytes(x, p, batch), b = paged_attn_bytes(p, q_heads);
   return ((a > b ? a : b) + 255) / 256 * 256;
@@ -150,9 +158,7 @@ fl_status fl_paged_read(const fl_paged_index* index, const fl_paged_pool* pool, 
   if (!place || !aligned(place, 4) || !k || !v || !aligned(k, 16) || !aligned(v, 16) ||
       !good_strides(token_stride, head_stride, 8))
     return FL_ERR_INVALID;
-  // rows that overlap would be written by several warps at once
-  if ((n_tokens > 1 && token_stride < FL_HEAD_DIM) || (pool->kv_heads > 1 && head_stride < FL_HEAD_DIM))
-    return FL_ERR_INVALID;
+  if (!rows_apart(n_tokens, token_stride, pool->kv_heads, head_stride)) return FL_ERR_INVALID;
   PagedReadArgs a{*index, *pool, n_tokens, place, k, v, token_stride, head_stride};
   return launched(launch_paged_read(a, (cudaStream_t)stream));
 }
@@ -197,9 +203,7 @@ fl_status fl_paged_attn_decode(const fl_paged_index* index, const fl_paged_pool*
   if (batch == 0) return FL_OK;
   if (!o || !aligned(o, 16) || !good_strides(o_batch_stride, o_head_stride, 4) || !aligned(lse, 4))
     return FL_ERR_INVALID;
-  // rows that overlap would be written by several CTAs at once
-  if ((batch > 1 && o_batch_stride < FL_HEAD_DIM) || (q_heads > 1 && o_head_stride < FL_HEAD_DIM))
-    return FL_ERR_INVALID;
+  if (!rows_apart(batch, o_batch_stride, q_heads, o_head_stride)) return FL_ERR_INVALID;
   a.sel = const_cast<int32_t*>(sel);
   a.keep = sel ? keep : 0;
   a.o = o;

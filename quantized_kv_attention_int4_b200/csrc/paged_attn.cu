@@ -285,7 +285,7 @@ struct Query {
       const int g = 4 * t + (i >> 1);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        raw[t][q] = g < live ? ldg_u4(a.q + (int64_t)b * a.q_batch_stride + (int64_t)(head0 + g) * a.q_head_stride + 32 * q + 8 * j)
+        raw[t][q] = g < live ? ld_u4(a.q + (int64_t)b * a.q_batch_stride + (int64_t)(head0 + g) * a.q_head_stride + 32 * q + 8 * j)
                              : make_uint4(0u, 0u, 0u, 0u);
     }
   }
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
   __syncthreads();
   // the line of units, then this CTA's and this warp's stretch of it
   auto length_of = [&](int b, bool tell) {  // -1: padded
-    const int s = a.slots ? __ldg(a.slots + b) : b;
+    const int s = a.slots ? ld(a.slots + b) : b;
     if (s < 0 || s >= a.x.slots) {
       if (s != -1 && tell) errors.add(FL_DEV_SLOT_RANGE, b);
       return -1;
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
     return;
   }
   if (wlo < whi) {
-    use.slot = a.slots ? __ldg(a.slots + use.b) : use.b;
+    use.slot = a.slots ? ld(a.slots + use.b) : use.b;
     line.place(use, use.n);
     const int seg = left / use.units;
     use.u = left - seg * use.units;
@@ -805,10 +805,10 @@ __global__ void __launch_bounds__(Shape<kTiles>::kThreads, 1)
           rows = -1;
           int block = load.u + lane;
           if (block < load.np) {
-            if (kSel) block = __ldg(a.sel + ((size_t)load.b * heads + load.h) * a.keep + block);
+            if (kSel) block = ld(a.sel + ((size_t)load.b * heads + load.h) * a.keep + block);
             int error = 0;
             if (!kSel || (block >= 0 && block < paged_full(load.n))) {
-              const int page = __ldg(a.x.table + (int64_t)load.slot * a.x.max_pages + block);
+              const int page = ld(a.x.table + (int64_t)load.slot * a.x.max_pages + block);
               if (page >= 0 && page < a.x.pages) rows = (page * heads + load.h) * (kRec / 128);
               else error = FL_DEV_PAGE_RANGE;
             } else if (block != -1) {

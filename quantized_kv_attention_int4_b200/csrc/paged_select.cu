@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
   auto page_of = [&](const At& p) {
     const int block = p.c * kChunk + (tid >> 2);
     if (block >= p.full) return -1;
-    const int page = __ldg(x.table + (int64_t)p.slot * x.max_pages + block);
+    const int page = ld(x.table + (int64_t)p.slot * x.max_pages + block);
     if (page >= 0 && page < x.pages) return page;
     if (j == 0) paged_error(x, FL_DEV_PAGE_RANGE, p.b);
     return -1;
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
   }
   uint4 sz[8];
 #pragma unroll
-  for (int m = 0; m < 8; ++m) sz[m] = ldg_u4(scales(cur, page) + 64 * m);
+  for (int m = 0; m < 8; ++m) sz[m] = ld_u4(scales(cur, page) + 64 * m);
   int staged_b = -1, staged_h = -1;
   for (; w < end; ++w) {
     At after = ahead;
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kST, 2) score_kernel(PagedAttnArgs a) {
             mma_f64(sum[2 * y + 1], __hiloint2double((int)((v & 0x7fffu) << 10), 0), y ? p.y : p.x);
             over |= (v & 0x7fff7fffu) + 0x04000400u;
           }
-          if (t == 2 && rec1 && g0 + 8 >= a.group) sz[m] = ldg_u4(rec1 + 64 * m);
+          if (t == 2 && rec1 && g0 + 8 >= a.group) sz[m] = ld_u4(rec1 + 64 * m);
         }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {

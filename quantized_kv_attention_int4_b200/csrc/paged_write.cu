@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kAT, 3) append_kernel(PagedAppendArgs a) {
   const int copies = (heads + 15) / 16;
   const int items = paged_scan<kAT>(a.batch, prefix, sm.red, [&](int b) {
     const int s = paged_slot(x, a.slots, b, tell);
-    const int c = __ldg(a.start + b), r0 = __ldg(a.cu + b), r1 = __ldg(a.cu + b + 1);
+    const int c = ld(a.start + b), r0 = ld(a.cu + b), r1 = ld(a.cu + b + 1);
     if (s < 0 || c < 0 || r1 == r0) return 0;
     if (r0 < 0 || r1 < r0 || r1 > a.n_tokens) {
       if (tell) paged_error(x, FL_DEV_COUNT, b);
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kAT, 3) append_kernel(PagedAppendArgs a) {
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const int b = paged_find(prefix, a.batch, item), left = item - prefix[b];
     const int s = paged_slot(x, a.slots, b, false);
-    const int c = __ldg(a.start + b), row0 = __ldg(a.cu + b), n = c + __ldg(a.cu + b + 1) - row0;
+    const int c = ld(a.start + b), row0 = ld(a.cu + b), n = c + ld(a.cu + b + 1) - row0;
     const int full0 = paged_full(c), full1 = paged_full(n);
     if (full0 == full1) {
       const int h0 = 16 * left, hn = min(16, heads - h0);
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kAT, 3) append_kernel(PagedAppendArgs a) {
 // rows l / 16, l / 16 + 2, ....  Rows of one page in order, the usual case, are read all at once;
 // otherwise one after the other, the key scales staying in registers while the page does not
 // change.
-constexpr int kReadRows = 16, kReadWarps = 8;
+constexpr int kReadRows = 16, kReadWarps = 8, kReadAhead = 4;
 
 __device__ __forceinline__ uint32_t bf2(float a, float b) {
   __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
@@ -249,12 +249,12 @@ __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(PagedReadArgs a) 
   grid_dep_wait();
   if (run * kReadRows >= a.n_tokens) return;
   const int cl = lane & 15, half = lane >> 4;
-  const int mine = lane < kReadRows && t0 + lane < a.n_tokens ? __ldg(a.place + t0 + lane) : -1;
+  const int mine = lane < kReadRows && t0 + lane < a.n_tokens ? ld(a.place + t0 + lane) : -1;
   const int page_end = a.x.pages, all_end = a.x.pages + a.x.slots;
   const int64_t out = (int64_t)t0 * a.token_stride + (int64_t)h * a.head_stride + 8 * cl;
   float2 ksz[8];
   auto key_scales = [&](const uint8_t* rec) {
-    const uint4 s0 = ldg_u4(rec + kRecKsz + 32 * cl), s1 = ldg_u4(rec + kRecKsz + 32 * cl + 16);
+    const uint4 s0 = ld_u4(rec + kRecKsz + 32 * cl), s1 = ld_u4(rec + kRecKsz + 32 * cl + 16);
     const uint32_t w[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e) ksz[e] = unpack_sz(w[e]);
@@ -276,16 +276,19 @@ __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(PagedReadArgs a) 
     const uint8_t* rec = a.p.rec + ((size_t)page0 * heads + h) * kRec;
     const int row0 = (at0 & 63) + half;
     key_scales(rec);
-    uint32_t kw[kReadRows / 2], vw[kReadRows / 2], vz[kReadRows / 2];
 #pragma unroll
-    for (int i = 0; i < kReadRows / 2; ++i) {
-      const uint32_t* row = reinterpret_cast<const uint32_t*>(rec + (row0 + 2 * i) * 128);
-      kw[i] = __ldg(row + cl);
-      vw[i] = __ldg(row + 16 + cl);
-      vz[i] = __ldg(reinterpret_cast<const uint32_t*>(rec + kRecVsz) + 2 * (row0 + 2 * i) + (cl >> 3));
+    for (int i0 = 0; i0 < kReadRows / 2; i0 += kReadAhead) {
+      uint32_t kw[kReadAhead], vw[kReadAhead], vz[kReadAhead];
+#pragma unroll
+      for (int i = 0; i < kReadAhead; ++i) {
+        const uint32_t* row = reinterpret_cast<const uint32_t*>(rec + (row0 + 2 * (i0 + i)) * 128);
+        kw[i] = ld(row + cl);
+        vw[i] = ld(row + 16 + cl);
+        vz[i] = ld(reinterpret_cast<const uint32_t*>(rec + kRecVsz) + 2 * (row0 + 2 * (i0 + i)) + (cl >> 3));
+      }
+#pragma unroll
+      for (int i = 0; i < kReadAhead; ++i) put(2 * (i0 + i) + half, kw[i], vw[i], vz[i]);
     }
-#pragma unroll
-    for (int i = 0; i < kReadRows / 2; ++i) put(2 * i + half, kw[i], vw[i], vz[i]);
     return;
   }
   int cur = -1;
@@ -301,15 +304,15 @@ __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(PagedReadArgs a) 
     if (page < page_end) {
       const uint8_t* rec = a.p.rec + ((size_t)page * heads + h) * kRec;
       const uint32_t* words = reinterpret_cast<const uint32_t*>(rec + row * 128);
-      const uint32_t kw = __ldg(words + cl), vw = __ldg(words + 16 + cl);
-      const uint32_t vz = __ldg(reinterpret_cast<const uint32_t*>(rec + kRecVsz) + 2 * row + (cl >> 3));
+      const uint32_t kw = ld(words + cl), vw = ld(words + 16 + cl);
+      const uint32_t vz = ld(reinterpret_cast<const uint32_t*>(rec + kRecVsz) + 2 * row + (cl >> 3));
       if (page != cur) key_scales(rec);
       cur = page;
       put(r, kw, vw, vz);
     } else {
       const size_t off = (((size_t)(page - page_end) * heads + h) * FL_PAGE + row) * kD + 8 * cl;
-      __stcs(reinterpret_cast<uint4*>(a.k + out + r * a.token_stride), ldg_u4(a.p.tail_k + off));
-      __stcs(reinterpret_cast<uint4*>(a.v + out + r * a.token_stride), ldg_u4(a.p.tail_v + off));
+      __stcs(reinterpret_cast<uint4*>(a.k + out + r * a.token_stride), ld_u4(a.p.tail_k + off));
+      __stcs(reinterpret_cast<uint4*>(a.v + out + r * a.token_stride), ld_u4(a.p.tail_v + off));
     }
   }
 }

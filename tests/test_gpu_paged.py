@@ -480,6 +480,73 @@ def test_a_captured_step_replays_on_grown_requests():
     assert c.status()[2] == 0
 
 
+def test_captured_calls_behind_copies_and_joined_streams():
+    """Captured behind a memory set, with two streams forked and joined (each with a workspace and a
+    plane of its own), and replayed: the calls' programmatic launches keep every dependency."""
+    g = gen(21)
+    pair, slots = filled([700, 64, 130], 2, 4, g)
+    c = pair.c
+    other = paged.PagedPool.empty(c.index, 2)
+    other.rec.copy_(c.pools[0].rec)
+    other.tail_k.copy_(c.pools[0].tail_k), other.tail_v.copy_(c.pools[0].tail_v)
+    ws2 = paged.workspace(c.index, other, 3, 8)
+    sl = i32(slots)
+    q = bf16(g, 3, 8, D, scale=1.5).cuda()
+    ref, sref = c.attend(0, sl, q), c.attend(0, sl, q, keep=3)
+    o1, o2, o3 = (torch.empty_like(ref) for _ in range(3))
+    sel = torch.full((3, 2, 3), -1, dtype=torch.int32, device="cuda")
+    place = torch.empty(64, dtype=torch.int32, device="cuda")
+    k, v = torch.empty(64, 2, D, dtype=torch.bfloat16, device="cuda"), torch.empty(64, 2, D, dtype=torch.bfloat16, device="cuda")
+    begin, cu = i32([3, 0, 0]), i32([0, 64, 64, 64])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        paged.fl_paged_workspace_init(c.ws)
+        o1.zero_()
+        paged.fl_paged_attn_decode(c.index, c.pools[0], sl, q, o1, c.ws)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            paged.fl_paged_attn_decode(c.index, other, sl, q, o2, ws2)
+            paged.fl_paged_slot_map(c.index, sl, begin, cu, place, None)
+        paged.fl_paged_select(c.index, c.pools[0], sl, q, sel, c.ws)
+        main.wait_stream(side)
+        paged.fl_paged_read(c.index, other, place, k, v)
+        paged.fl_paged_attn_decode(c.index, c.pools[0], sl, q, o3, c.ws, sel=sel)
+    rows = torch.from_numpy(pair.o.keys_values(slots[0], 1)[0][3:67].astype(np.float32)).bfloat16()
+    for _ in range(3):
+        for t in (o1, o2, o3, k, v):
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o1, ref) and torch.equal(o2, ref) and torch.equal(o3, sref)
+        assert torch.equal(k[:, 1].cpu(), rows)
+
+
+def test_many_entries_take_the_other_scan():
+    """Beyond 128 entries a call scans its lengths block-wide: the same results, padded entries
+    and requests of no tokens among them."""
+    g = gen(22)
+    r = np.random.default_rng(22)
+    lengths = [int(n) for n in r.integers(0, 150, 300)]
+    pair, slots = filled(lengths, 1, 2, g)
+    q = bf16(g, 300, 2, D)
+    o, lse = torch.empty(300, 2, D, device="cuda"), torch.empty(300, 2, device="cuda")
+    named = np.array(slots)
+    named[r.random(300) < 0.1] = -1
+    o.fill_(7.0), lse.fill_(7.0)
+    pair.c.attend(0, i32(named), q.cuda(), o, lse)
+    live = [i for i in range(300) if named[i] >= 0]
+    check_attention(pair, named[live], q[live], o[live], lse[live])
+    assert (o[named < 0] == 7).all() and (lse[named < 0] == 7).all()
+    first = torch.empty(100, 2, D, device="cuda")   # a part of it through the other path
+    pair.c.attend(0, i32(slots[:100]), q[:100].cuda(), first)
+    second = torch.empty(300, 2, D, device="cuda")
+    pair.c.attend(0, i32(slots), q.cuda(), second)
+    assert torch.allclose(first, second[:100], rtol=1e-5, atol=1e-6)
+
+
 def test_calls_on_a_stream_of_their_own():
     g = gen(20)
     pair, slots = filled([500, 90], 2, 2, g)

@@ -118,7 +118,8 @@ def test_append_and_read_check_their_arguments():
     rd = lambda t=4, pl=FAKE, k=FAKE, v=FAKE, ts=256, hs=128: paged._c_read(  # noqa: E731
         ref(x), ref(p), t, pl, k, v, ts, hs, None)
     assert rd(t=-1) == rd(pl=None) == rd(k=None) == rd(v=FAKE + 2) == abi.FL_ERR_INVALID
-    assert rd(ts=64) == rd(hs=64) == abi.FL_ERR_INVALID         # output rows would overlap
+    assert rd(ts=64) == rd(hs=64) == rd(ts=128) == rd(ts=248) == abi.FL_ERR_INVALID   # output rows would overlap
+    assert rd(ts=128, hs=504) == abi.FL_ERR_INVALID             # head by head: four rows of 128 reach into the next head
     assert rd(t=0) == abi.FL_OK
 
 
@@ -132,6 +133,7 @@ def test_attention_and_selection_check_their_arguments():
     assert att(hq=3) == att(hq=0) == abi.FL_ERR_INVALID          # not a multiple of the key-value heads
     assert att(q=None) == att(q=FAKE + 8) == att(qb=500) == att(qh=-128) == abi.FL_ERR_INVALID
     assert att(o=None) == att(o=FAKE + 4) == att(ob=510) == att(oh=64) == att(ob=64) == abi.FL_ERR_INVALID
+    assert att(ob=128) == att(ob=128, oh=376) == att(ob=508) == abi.FL_ERR_INVALID   # rows of two entries would overlap
     assert att(lse=FAKE + 2) == abi.FL_ERR_INVALID
     assert att(sel=FAKE, keep=0) == att(sel=FAKE + 1, keep=2) == abi.FL_ERR_INVALID
     assert att(sel=FAKE, keep=paged.MAX_KEEP + 1) == abi.FL_ERR_UNSUPPORTED
