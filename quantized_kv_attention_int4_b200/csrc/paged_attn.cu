@@ -21,8 +21,8 @@
 //   the exponent of 1024 is the binary16 number 1024 + n (1024 + 16 n at bits 4..7), so one
 //   logic and one packed fp16 operation turn two codes into two operands n - 8, exactly.  q_c
 //   has 8 significant bits and s_c 11, so q_c s_c is two binary16 parts exactly: hi = fl(q s),
-//   lo = fma(q, s, -hi); they fill columns 2j and 2j + 1 of query head j.  Powers of two keep
-//   both in range: q is scaled per head, s per record.  The second sum is one more product
+//   lo = fma(q, s, -hi); they fill columns 2j and 2j + 1 of query head j.  A power of two on q,
+//   changed when a record's scales need it, keeps both in range.  The second sum is one more product
 //   whose rows are all z, and then all 8.
 //   o_c = sum_t (p_t s_t) (n_tc - 8) + sum_t p_t (z_t + 8 s_t) per 64-channel half.  p s goes
 //   in two binary16 parts as well (2^-22 relative), the second sum in fp32.
@@ -30,8 +30,8 @@
 //   their range keep partial sums small (with 0..15, whose products and zero points cancel,
 //   outputs over 8000 tokens were off by 1.7e-4), and a block's sums are added to the running
 //   ones in ordinary fp32.
-//   The running maximum is raised only when a score passes it by 8 (base 2): sums stay far
-//   inside fp32 and the accumulators are hardly ever rescaled.
+//   Weights are relative to a number that is raised only when p s would leave binary16's range,
+//   and then by 8 (base 2) more than needed: the accumulators are hardly ever rescaled.
 //   Tail rows are BF16: q.k exactly so, p in three BF16 parts (2^-24).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -216,7 +216,8 @@ struct Errors {
 template <int kTiles>
 struct State {
   float acc[8][kTiles][4];  // [2 q + f]: rows i: channel 32 q + 4 i + 2 f, rows i + 8: the next
-  float m[kTiles], l[kTiles], z0[kTiles], z1[kTiles];  // max (all lanes of a head), this lane's sums
+  // weights are p = 2^(score - m), m one number for all lanes of a head; this lane's sums
+  float m[kTiles], l[kTiles], z0[kTiles], z1[kTiles];
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -229,18 +230,19 @@ struct State {
       l[t] = z0[t] = z1[t] = 0.f;
     }
   }
-  // Raise the maxima to cover the unit's (top[t]: this lane's highest score of its head).
-  __device__ __forceinline__ void raise(const float (&top)[kTiles]) {
+  // Raise m so that no weight of a unit whose scores reach top[t] (this lane's, of its head)
+  // passes 2^most; then the largest is 2^(most - 8), so that m rarely moves again.
+  __device__ __forceinline__ void raise(const float (&top)[kTiles], float most) {
     bool over = false;
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) over |= top[t] > m[t] + 8.f;
+    for (int t = 0; t < kTiles; ++t) over |= top[t] > m[t] + most;
     if (!__any_sync(kFull, over)) return;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
       float x = top[t];
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-      const float mn = fmaxf(m[t], x), f = mn == m[t] ? 1.f : ex2(m[t] - mn);
+      const float mn = fmaxf(m[t], x - (most - 8.f)), f = mn == m[t] ? 1.f : ex2(m[t] - mn);
       m[t] = mn;
       l[t] *= f;
       z0[t] *= f;
@@ -269,12 +271,14 @@ __device__ __forceinline__ uint32_t centred(uint32_t x) {
 }
 
 // The queries of a segment: lane (i, j) holds, for column i of each tile (head i / 2, part i
-// % 2), channels 32 q + 8 j + {0, 4}, {1, 5}, {2, 6}, {3, 7} scaled to [2^5, 2^6) at most.
+// % 2), channels 32 q + 8 j + {0, 4}, {1, 5}, {2, 6}, {3, 7} times a power of two: the largest in
+// [2^shift, 2^(shift + 1)).
 template <int kTiles>
 struct Query {
   uint32_t w[kTiles][16];  // [4 q + pair]
   float scale[kTiles];     // of head j (not i / 2): scores in base 2 = scaled dot times this
   uint32_t part;           // all ones in the lanes of part 1
+  int shift;
   uint4 raw[kTiles][4];    // as read
 
   // Start the loads; prepare() waits for them.
@@ -292,6 +296,7 @@ struct Query {
   __device__ __forceinline__ void prepare() {
     const int lane = threadIdx.x & 31, i = lane >> 2, j = lane & 3;
     part = i & 1 ? 0xffffffffu : 0u;
+    shift = 5;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
       const uint4(&x)[4] = raw[t];
@@ -319,20 +324,34 @@ struct Query {
       scale[t] = __shfl_sync(kFull, back, 8 * j) * kQScale;
     }
   }
+  // Fit the shift to a record whose largest scale has exponent field ek (below 2^(ek - 14)):
+  // products q s stay below 2^15, and where they can above 2^3, far from binary16's last bit
+  // 2^-24.  Rarely changes: records' scales are much alike.
+  __device__ __forceinline__ void fit(int ek) {
+    if (shift + ek <= 28 && (shift + ek >= 18 || shift == 14)) return;
+    const int by = min(14, 25 - ek) - shift, a = by / 2, b = by - a;
+    shift += by;
+    const uint32_t fa = (uint32_t)(15 + a) * 0x04000400u, fb = (uint32_t)(15 + b) * 0x04000400u;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      scale[t] *= pow2i(-by);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) w[t][k] = u2(__hmul2(__hmul2(h2(w[t][k]), h2(fa)), h2(fb)));
+    }
+  }
 };
 
 // One record in shared memory (swizzled rows of 128 bytes).
 template <int kTiles>
-__device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr, State<kTiles>& s) {
+__device__ __forceinline__ void block_unit(unsigned st, Query<kTiles>& qr, State<kTiles>& s) {
   const int lane = threadIdx.x & 31, i = lane >> 2, j = lane & 3;
   // largest key and value scales: 4 words a lane, scales in the low halves
   const uint4 kw = lds128(st + (68 + (lane >> 3)) * 128 + (((lane & 7) ^ (4 + (lane >> 3))) << 4));
   const uint4 vw = lds128(st + (64 + (lane >> 3)) * 128 + (((lane & 7) ^ (lane >> 3)) << 4));
-  const uint32_t ktop = __reduce_max_sync(kFull, max(max(kw.x << 16, kw.y << 16), max(kw.z << 16, kw.w << 16)));
-  const uint32_t vtop = __reduce_max_sync(kFull, max(max(vw.x << 16, vw.y << 16), max(vw.z << 16, vw.w << 16)));
-  // keys' scales times 2^(23 - ek): the largest in [2^8, 2^9); 8 in those units is 2^(ek - 20)
-  const int ek = max((int)(ktop >> 26) & 31, 8);
-  const uint32_t up = (uint32_t)(38 - ek) * 0x04000400u, eight = (uint32_t)(ek - 5) * 0x04000400u;
+  const uint32_t ktop = __reduce_max_sync(kFull, __vmaxu2(__vmaxu2(kw.x, kw.y), __vmaxu2(kw.z, kw.w)) << 16);
+  const uint32_t vtop = __reduce_max_sync(kFull, __vmaxu2(__vmaxu2(vw.x, vw.y), __vmaxu2(vw.z, vw.w)) << 16);
+  qr.fit((int)(ktop >> 26) & 31);
+  constexpr uint32_t eight = 0x48004800u;
 
   // ---- scores: 64 tokens x 8 columns a tile, two chains of four products each
   float c[4][kTiles][4], zc[kTiles][4];
@@ -349,7 +368,7 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
       uint32_t sp[4], zp[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        sp[k] = u2(__hmul2(h2(__byte_perm((&w0.x)[k], (&w1.x)[k], 0x5410)), h2(up)));
+        sp[k] = __byte_perm((&w0.x)[k], (&w1.x)[k], 0x5410);
         zp[k] = __byte_perm((&w0.x)[k], (&w1.x)[k], 0x7632);
       }
       uint32_t bq[kTiles][4];
@@ -393,11 +412,10 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
 #pragma unroll
         for (int k = 0; k < 4; ++k) c[r][t][k] = hq == 0 ? d[r][t][k] : c[r][t][k] + d[r][t][k];
   }
-  // lane (i, j): tokens 16 r + i and 16 r + 8 + i of head j; a score is sum f + base, f >= 0
-  float top[kTiles], f[kTiles], off[kTiles];
+  // lane (i, j): tokens 16 r + i and 16 r + 8 + i of head j; a score is sum scale + off, scale >= 0
+  float top[kTiles], off[kTiles];
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
-    f[t] = qr.scale[t] * pow2i(ek - 23);
     off[t] = (zc[t][0] + zc[t][3]) * qr.scale[t];
     float mx = -INFINITY;
 #pragma unroll
@@ -406,14 +424,12 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
       c[r][t][1] = c[r][t][2] + c[r][t][3];
       mx = fmaxf(mx, fmaxf(c[r][t][0], c[r][t][1]));
     }
-    top[t] = fmaf(mx, f[t], off[t]);
+    top[t] = fmaf(mx, qr.scale[t], off[t]);
   }
-  s.raise(top);
+  // values' scales are below 2^(ev - 14): p s < 2^15
+  s.raise(top, 29.f - (float)max((int)(vtop >> 26) & 31, 1));
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) off[t] -= s.m[t];
-  // values' scales times 2^(21 - ev): the largest in [2^6, 2^7), so that p s < 2^15
-  const int ev = max((int)(vtop >> 26) & 31, 1);
-  const float pe = pow2i(21 - ev), back = pow2i(ev - 21);
   uint32_t bv[kTiles][2][8];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
@@ -424,13 +440,12 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
       const float c0 = fmaf(8.f, f0.x, f0.y), c1 = fmaf(8.f, f1.x, f1.y);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        const float p = ex2(fmaf(c[r][t][k], f[t], off[t]));
+        const float p = ex2(fmaf(c[r][t][k], qr.scale[t], off[t]));
         s.l[t] += p;
         s.z0[t] = fmaf(p, c0, s.z0[t]);
         s.z1[t] = fmaf(p, c1, s.z1[t]);
-        const float w = p * pe;
-        bv[t][0][2 * r + k] = transpose8(split_f16(w * f0.x));
-        bv[t][1][2 * r + k] = transpose8(split_f16(w * f1.x));
+        bv[t][0][2 * r + k] = transpose8(split_f16(p * f0.x));
+        bv[t][1][2 * r + k] = transpose8(split_f16(p * f1.x));
       }
     }
 #pragma unroll
@@ -463,7 +478,7 @@ __device__ __forceinline__ void block_unit(unsigned st, const Query<kTiles>& qr,
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s.acc[2 * q + f][t][k] = fmaf(d[f][t][k], back, s.acc[2 * q + f][t][k]);
+        for (int k = 0; k < 4; ++k) s.acc[2 * q + f][t][k] += d[f][t][k];
   }
 }
 
@@ -510,7 +525,7 @@ __device__ __forceinline__ void tail_unit(unsigned st, int live, const Query<kTi
     c[t][1] = i + 8 < live ? c[t][2] * qr.scale[t] : -INFINITY;
     top[t] = fmaxf(c[t][0], c[t][1]);
   }
-  s.raise(top);
+  s.raise(top, 24.f);
   uint32_t bv[kTiles][2][2];
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
