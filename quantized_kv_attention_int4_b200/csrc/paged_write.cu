@@ -14,7 +14,8 @@ namespace {
 //
 // 256 threads: thread t owns channels 8 (t % 16) .. + 7 of rows t / 16 + 16 i, i = 0..3, of
 // keys and values (16-byte loads, 256-byte rows).  A value group (row, 64-channel half) is
-// eight neighbouring threads: three shuffles.  A key group (channel) is 64 rows: four in the
+// eight neighbouring threads: three steps of shuffles, after which each pair of threads has one
+// of the four rows and computes its scale and zero for all eight.  A key group (channel) is 64 rows: four in the
 // thread, two row sets in the warp, eight warps through shared memory.  Minima and maxima are
 // taken on the BF16 values, exact.
 constexpr int kAT = 256;
@@ -46,32 +47,68 @@ __device__ __noinline__ uint32_t quant_word_exact(uint4 x, uint4 sz0, uint4 sz1)
   return w;
 }
 
-// The same with the rounded division taken only near a half.  With r = 1 / s to 2^-23,
-// |d r - d / s| <= 2.9e-6 for codes up to 16 (beyond, both clamp), and the rounded quotient is
-// within 2^-20 of d / s, so away from a half by 1e-4 all of them round to the same code.
-// Rounding is an addition of 1.5 2^23 (conversions are issued at a quarter of its rate): the
-// sum's low bits are the code.  NaN, which an infinity gives, clamps to 0 as there.
-__device__ __forceinline__ uint32_t quant_word(uint4 x, const float2* sz, const float* rcp, uint4 sz0, uint4 sz1) {
-  constexpr float kMagic = 12582912.f;
-  float f[8], worst = 0.f;
-  bf16x8(x, f);
-  uint32_t w = 0;
-#pragma unroll
-  for (int e = 7; e >= 0; --e) {
-    const float t = fminf(fmaxf(__fsub_rn(f[e], sz[e].y) * rcp[e], 0.f), 15.f);
-    const float up = __fadd_rn(t, kMagic);
-    worst = fmaxf(worst, fabsf(__fsub_rn(t, __fsub_rn(up, kMagic))));
-    w = (w << 4) + (__float_as_uint(up) & 15u);
-  }
-  if (worst >= 0.4999f) w = quant_word_exact(x, sz0, sz1);
-  return w;
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n.reg .b64 a, b, c;\n"
+      "mov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 a, a, b, c;\nmov.b64 {%0, %1}, a;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n.reg .b64 a, b;\n"
+      "mov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\n"
+      "add.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float mul_sat(float a, float b) {
+  float d;
+  asm("mul.rn.sat.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
-// 1 / s to 2^-23, and 0 for s = 0 (whose code is 0); binary16 scales are at least 2^-24.
+// The same with the rounded division taken only near a half.  u = (x - z) r / 15, cut off to
+// [0, 1], with r / 15 to 2^-22, so 15 u is d / s to 1e-5 for codes up to 16 (beyond, both clamp),
+// and the rounded quotient is within 2^-20 of d / s: away from a half by 1e-4 all of them round
+// to the same code.  Cutting off is free in the product, and gives 0 for the NaN of an infinity,
+// as there.  Rounding is an addition of 1.5 2^23, after which four codes add up to 16 bits
+// exactly: no conversions, which issue at a quarter of the rate, and no shifts.
+// nz = -z of the channel pairs, r15 = r / 15.
+__device__ __forceinline__ uint32_t quant_word(uint4 x, const float2* nz, const float2* r15, uint4 sz0, uint4 sz1) {
+  constexpr float kMagic = 12582912.f;
+  const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+  const float2 c15 = make_float2(15.f, 15.f), magic = make_float2(kMagic, kMagic), back = make_float2(-kMagic, -kMagic);
+  float worst = 0.f;
+  float2 code[4], up[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 d = add2(make_float2(bf16_lo(xs[e]), bf16_hi(xs[e])), nz[e]);
+    const float2 u = make_float2(mul_sat(d.x, r15[e].x), mul_sat(d.y, r15[e].y));
+    up[e] = fma2(u, c15, magic);
+    code[e] = add2(up[e], back);
+    const float2 off = fma2(u, c15, make_float2(-code[e].x, -code[e].y));
+    worst = fmaxf(worst, fmaxf(fabsf(off.x), fabsf(off.y)));
+  }
+  uint32_t half[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 c256 = make_float2(256.f, 256.f);
+    const float2 two = fma2(code[2 * i + 1], c256, make_float2(up[2 * i].x, code[2 * i].y));
+    half[i] = __float_as_uint(fmaf(two.y, 16.f, two.x));
+  }
+  if (worst >= 0.4999f) return quant_word_exact(x, sz0, sz1);
+  return __byte_perm(half[0], half[1], 0x5410);
+}
+
+// 1 / (15 s) to 2^-22, and 0 for s = 0 (whose code is 0); binary16 scales are at least 2^-24.
 __device__ __forceinline__ float rcp_scale(float s) {
   float r;
   asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
-  return s == 0.f ? 0.f : r;
+  return s == 0.f ? 0.f : r * (1.f / 15.f);
 }
 
 __global__ void __launch_bounds__(kAT, 3) append_kernel(PagedAppendArgs a) {
@@ -177,35 +214,55 @@ __global__ void __launch_bounds__(kAT, 3) append_kernel(PagedAppendArgs a) {
       {
         const uint4 s0 = *reinterpret_cast<const uint4*>(&sm.sz[8 * chunk]);
         const uint4 s1 = *reinterpret_cast<const uint4*>(&sm.sz[8 * chunk + 4]);
-        const float2 sz[8] = {unpack_sz(s0.x), unpack_sz(s0.y), unpack_sz(s0.z), unpack_sz(s0.w),
-                              unpack_sz(s1.x), unpack_sz(s1.y), unpack_sz(s1.z), unpack_sz(s1.w)};
-        float rcp[8];
+        const uint32_t w[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        float2 nz[4], r15[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) rcp[e] = rcp_scale(sz[e].x);
+        for (int e = 0; e < 4; ++e) {
+          const float2 a0 = unpack_sz(w[2 * e]), a1 = unpack_sz(w[2 * e + 1]);
+          nz[e] = make_float2(-a0.y, -a1.y);
+          r15[e] = make_float2(rcp_scale(a0.x), rcp_scale(a1.x));
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint32_t*>(rec + (r0 + 16 * i) * 128 + 4 * chunk) = quant_word(k4[i], sz, rcp, s0, s1);
+          *reinterpret_cast<uint32_t*>(rec + (r0 + 16 * i) * 128 + 4 * chunk) = quant_word(k4[i], nz, r15, s0, s1);
+      }
+      // values: each step of the reduction halves the rows a thread still answers for
+      uint32_t lo[4], hi[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[i] = bmin2(bmin2(v4[i].x, v4[i].y), bmin2(v4[i].z, v4[i].w));
+        hi[i] = bmax2(bmax2(v4[i].x, v4[i].y), bmax2(v4[i].z, v4[i].w));
+      }
+#pragma unroll
+      for (int o = 4; o; o >>= 1) {
+        const bool up = lane & o;
+        const int rows = o == 4 ? 2 : 1;
+#pragma unroll
+        for (int i = 0; i < rows; ++i) {
+          const int other = i + (o > 1 ? rows : 0);
+          const uint32_t l = __shfl_xor_sync(kFull, up ? lo[i] : lo[other], o);
+          const uint32_t h2 = __shfl_xor_sync(kFull, up ? hi[i] : hi[other], o);
+          lo[i] = bmin2(up ? lo[other] : lo[i], l);
+          hi[i] = bmax2(up ? hi[other] : hi[i], h2);
+        }
+      }
+      uint32_t mine;
+      {
+        __half hs, hz;
+        group_sz(fminf(bf16_lo(lo[0]), bf16_hi(lo[0])), fmaxf(bf16_lo(hi[0]), bf16_hi(hi[0])), hs, hz);
+        mine = pack_sz(hs, hz);
+        const int row = r0 + 16 * ((lane >> 1) & 3);
+        if ((lane & 1) == 0) reinterpret_cast<uint32_t*>(rec + kRecVsz)[2 * row + (chunk >> 3)] = mine;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t lo = bmin2(bmin2(v4[i].x, v4[i].y), bmin2(v4[i].z, v4[i].w));
-        uint32_t hi = bmax2(bmax2(v4[i].x, v4[i].y), bmax2(v4[i].z, v4[i].w));
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
-          lo = bmin2(lo, __shfl_xor_sync(kFull, lo, o));
-          hi = bmax2(hi, __shfl_xor_sync(kFull, hi, o));
-        }
-        __half hs, hz;
-        group_sz(fminf(bf16_lo(lo), bf16_hi(lo)), fmaxf(bf16_lo(hi), bf16_hi(hi)), hs, hz);
-        const int row = r0 + 16 * i;
-        const uint32_t both = pack_sz(hs, hz);
-        if ((chunk & 7) == 0)
-          reinterpret_cast<uint32_t*>(rec + kRecVsz)[2 * row + (chunk >> 3)] = both;
-        const float sv = __half2float(hs), zv = __half2float(hz), rv = rcp_scale(sv);
-        const float2 sz[8] = {{sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}, {sv, zv}};
-        const float rcp[8] = {rv, rv, rv, rv, rv, rv, rv, rv};
-        *reinterpret_cast<uint32_t*>(rec + row * 128 + 64 + 4 * chunk) =
-            quant_word(v4[i], sz, rcp, make_uint4(both, both, both, both), make_uint4(both, both, both, both));
+        const uint32_t both = __shfl_sync(kFull, mine, (lane & 24) + 2 * i);
+        const float2 f = unpack_sz(both);
+        const float rv = rcp_scale(f.x);
+        const float2 z2 = make_float2(-f.y, -f.y), r2 = make_float2(rv, rv);
+        const float2 nz[4] = {z2, z2, z2, z2}, r15[4] = {r2, r2, r2, r2};
+        *reinterpret_cast<uint32_t*>(rec + (r0 + 16 * i) * 128 + 64 + 4 * chunk) =
+            quant_word(v4[i], nz, r15, make_uint4(both, both, both, both), make_uint4(both, both, both, both));
       }
     }
     __syncthreads();  // every old tail row is in registers (and sm is free again)
