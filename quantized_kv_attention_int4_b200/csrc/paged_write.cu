@@ -18,7 +18,7 @@ namespace {
 // of the four rows and computes its scale and zero for all eight.  A key group (channel) is 64 rows: four in the
 // thread, two row sets in the warp, eight warps through shared memory.  Minima and maxima are
 // taken on the BF16 values, exact.
-constexpr int kAT = 256;
+constexpr int kAT = 256, kAppendCtas = 4;
 
 struct AppendSmem {
   uint32_t mn[8][64], mx[8][64];  // per warp and channel pair
@@ -77,8 +77,9 @@ __device__ __forceinline__ float mul_sat(float a, float b) {
 // to the same code.  Cutting off is free in the product, and gives 0 for the NaN of an infinity,
 // as there.  Rounding is an addition of 1.5 2^23, after which four codes add up to 16 bits
 // exactly: no conversions, which issue at a quarter of the rate, and no shifts.
-// nz = -z of the channel pairs, r15 = r / 15.
-__device__ __forceinline__ uint32_t quant_word(uint4 x, const float2* nz, const float2* r15, uint4 sz0, uint4 sz1) {
+// nz = -z of the channel pairs, r15 = r / 15; `close`: a code is to be taken from
+// quant_word_exact.
+__device__ __forceinline__ uint32_t quant_word(uint4 x, const float2* nz, const float2* r15, bool& close) {
   constexpr float kMagic = 12582912.f;
   const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
   const float2 c15 = make_float2(15.f, 15.f), magic = make_float2(kMagic, kMagic), back = make_float2(-kMagic, -kMagic);
@@ -100,7 +101,7 @@ __device__ __forceinline__ uint32_t quant_word(uint4 x, const float2* nz, const 
     const float2 two = fma2(code[2 * i + 1], c256, make_float2(up[2 * i].x, code[2 * i].y));
     half[i] = __float_as_uint(fmaf(two.y, 16.f, two.x));
   }
-  if (worst >= 0.4999f) return quant_word_exact(x, sz0, sz1);
+  close = worst >= 0.4999f;
   return __byte_perm(half[0], half[1], 0x5410);
 }
 
@@ -111,7 +112,7 @@ __device__ __forceinline__ float rcp_scale(float s) {
   return s == 0.f ? 0.f : r * (1.f / 15.f);
 }
 
-__global__ void __launch_bounds__(kAT, 3) append_kernel(PagedAppendArgs a) {
+__global__ void __launch_bounds__(kAT, kAppendCtas) append_kernel(PagedAppendArgs a) {
   extern __shared__ int32_t prefix[];
   __shared__ AppendSmem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(kAT, 3) append_kernel(PagedAppendArgs a) {
       return 0;
     }
     const int fill = paged_full(c + r1 - r0) - paged_full(c);
-    return fill ? fill * heads : copies;
+    return fill ? 2 * fill * heads : copies;
   });
   const int chunk = tid & 15, r0 = tid >> 4;
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
@@ -153,40 +154,31 @@ __global__ void __launch_bounds__(kAT, 3) append_kernel(PagedAppendArgs a) {
       }
       continue;
     }
-    const int j = left / heads, h = left - j * heads, block = full0 + j;
-    const size_t tail = ((size_t)s * heads + h) * FL_PAGE * kD;
-    uint16_t *tk = a.p.tail_k + tail, *tv = a.p.tail_v + tail;
-    int page = -1;
-    uint4 k4[4], v4[4];
-    {
-      page = x.table[(int64_t)s * x.max_pages + block];
-      if (page < 0 || page >= x.pages) {
-        if (tid == 0) paged_error(x, FL_DEV_PAGE_RANGE, b);
-        page = -1;
-      }
+    const bool values = left & 1;
+    const int j = (left >> 1) / heads, h = (left >> 1) - j * heads, block = full0 + j;
+    uint16_t* tail = (values ? a.p.tail_v : a.p.tail_k) + ((size_t)s * heads + h) * FL_PAGE * kD + 8 * chunk;
+    const uint16_t* rows = (values ? a.v : a.k) + (int64_t)(row0 - c) * a.token_stride + (int64_t)h * a.head_stride + 8 * chunk;
+    const int page = x.table[(int64_t)s * x.max_pages + block];
+    auto from = [&](int i) {
+      const int row = r0 + 16 * i, t = block * FL_PAGE + row;
+      return reinterpret_cast<const uint4*>(t < c ? tail + row * kD : rows + t * a.token_stride);
+    };
+    uint4 x4[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = r0 + 16 * i, t = block * FL_PAGE + row;
-        const uint16_t *ks, *vs;
-        if (t < c) {
-          ks = tk + row * kD;
-          vs = tv + row * kD;
-        } else {
-          const int64_t off = (int64_t)(row0 + t - c) * a.token_stride + (int64_t)h * a.head_stride;
-          ks = a.k + off;
-          vs = a.v + off;
-        }
-        k4[i] = *reinterpret_cast<const uint4*>(ks + 8 * chunk);
-        v4[i] = *reinterpret_cast<const uint4*>(vs + 8 * chunk);
-      }
-    }
-    if (page >= 0) {
-      uint8_t* rec = a.p.rec + ((size_t)page * heads + h) * kRec;
+    for (int i = 0; i < 4; ++i) x4[i] = *from(i);
+    const bool paged = page >= 0 && page < x.pages;
+    if (!paged && tid == 0) paged_error(x, FL_DEV_PAGE_RANGE, b);
+    uint8_t* rec = a.p.rec + ((size_t)(paged ? page : 0) * heads + h) * kRec;
+    auto code_at = [&](int i) {
+      return reinterpret_cast<uint32_t*>(rec + (r0 + 16 * i) * 128 + (values ? 64 : 0) + 4 * chunk);
+    };
+    unsigned again = 0;
+    if (paged && !values) {
       // keys: this thread's four rows, the warp's other row set, then the eight warps
       uint32_t mn[4], mx[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t p0 = (&k4[0].x)[e], p1 = (&k4[1].x)[e], p2 = (&k4[2].x)[e], p3 = (&k4[3].x)[e];
+        const uint32_t p0 = (&x4[0].x)[e], p1 = (&x4[1].x)[e], p2 = (&x4[2].x)[e], p3 = (&x4[3].x)[e];
         mn[e] = bmin2(bmin2(p0, p1), bmin2(p2, p3));
         mx[e] = bmax2(bmax2(p0, p1), bmax2(p2, p3));
         mn[e] = bmin2(mn[e], __shfl_xor_sync(kFull, mn[e], 16));
@@ -224,14 +216,25 @@ __global__ void __launch_bounds__(kAT, 3) append_kernel(PagedAppendArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint32_t*>(rec + (r0 + 16 * i) * 128 + 4 * chunk) = quant_word(k4[i], nz, r15, s0, s1);
+        {
+          bool close;
+          *code_at(i) = quant_word(x4[i], nz, r15, close);
+          again |= (unsigned)close << i;
+        }
       }
+      while (again) {
+        const int i = __ffs(again) - 1;
+        again &= again - 1;
+        *code_at(i) = quant_word_exact(*from(i), *reinterpret_cast<const uint4*>(&sm.sz[8 * chunk]),
+                                       *reinterpret_cast<const uint4*>(&sm.sz[8 * chunk + 4]));
+      }
+    } else if (paged) {
       // values: each step of the reduction halves the rows a thread still answers for
       uint32_t lo[4], hi[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        lo[i] = bmin2(bmin2(v4[i].x, v4[i].y), bmin2(v4[i].z, v4[i].w));
-        hi[i] = bmax2(bmax2(v4[i].x, v4[i].y), bmax2(v4[i].z, v4[i].w));
+        lo[i] = bmin2(bmin2(x4[i].x, x4[i].y), bmin2(x4[i].z, x4[i].w));
+        hi[i] = bmax2(bmax2(x4[i].x, x4[i].y), bmax2(x4[i].z, x4[i].w));
       }
 #pragma unroll
       for (int o = 4; o; o >>= 1) {
@@ -261,20 +264,26 @@ __global__ void __launch_bounds__(kAT, 3) append_kernel(PagedAppendArgs a) {
         const float rv = rcp_scale(f.x);
         const float2 z2 = make_float2(-f.y, -f.y), r2 = make_float2(rv, rv);
         const float2 nz[4] = {z2, z2, z2, z2}, r15[4] = {r2, r2, r2, r2};
-        *reinterpret_cast<uint32_t*>(rec + (r0 + 16 * i) * 128 + 64 + 4 * chunk) =
-            quant_word(v4[i], nz, r15, make_uint4(both, both, both, both), make_uint4(both, both, both, both));
+        bool close;
+        *code_at(i) = quant_word(x4[i], nz, r15, close);
+        again |= (unsigned)close << i;
+      }
+      if (__any_sync(kFull, again != 0)) {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t both = __shfl_sync(kFull, mine, (lane & 24) + 2 * i);
+          const uint4 sz = make_uint4(both, both, both, both);
+          if (again >> i & 1) *code_at(i) = quant_word_exact(*from(i), sz, sz);
+        }
       }
     }
-    __syncthreads();  // every old tail row is in registers (and sm is free again)
     if (j == 0) {
+      __syncthreads();  // every old tail row is in registers
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = r0 + 16 * i, t = full1 * FL_PAGE + row;
-        if (t >= c && t < n) {
-          const int64_t off = (int64_t)(row0 + t - c) * a.token_stride + (int64_t)h * a.head_stride + 8 * chunk;
-          *reinterpret_cast<uint4*>(tk + row * kD + 8 * chunk) = *reinterpret_cast<const uint4*>(a.k + off);
-          *reinterpret_cast<uint4*>(tv + row * kD + 8 * chunk) = *reinterpret_cast<const uint4*>(a.v + off);
-        }
+        if (t >= c && t < n)
+          *reinterpret_cast<uint4*>(tail + row * kD) = *reinterpret_cast<const uint4*>(rows + t * a.token_stride);
       }
     }
   }
@@ -380,8 +389,8 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
   // at most one item per entry and one more per 64 tokens
-  const int64_t items = ((int64_t)a.batch + a.n_tokens / FL_PAGE) * a.p.kv_heads;
-  const int grid = (int)(items < 3 * sms ? items : 3 * sms);
+  const int64_t items = 2 * ((int64_t)a.batch + a.n_tokens / FL_PAGE) * a.p.kv_heads;
+  const int grid = (int)(items < kAppendCtas * sms ? items : kAppendCtas * sms);
   return launch_pdl(append_kernel, dim3(grid), dim3(kAT), (size_t)(a.batch + 1) * 4, s, a);
 }
 
