@@ -5,11 +5,13 @@
 // ceil(c_i / 64); with P_i the sum of need over the valid entries up to i, entry i is granted
 // when need_i = 0 or P_i <= n_free, and its pages are free[n_free - 1 - (P_i - need_i) - j].
 // The granted entries that need pages are a prefix of the valid ones that do, so the stack
-// simply loses its top P and every entry's place on it is P_i - need_i.  One block does it (of
-// 128 threads up to 128 entries, where its barriers cost half of 1024 threads'): the work is a
-// scan over at most 8192 entries and 8 bytes per page, and its time is the launch and four
-// dependent trips to memory.  The kernels here start while their predecessor ends (programmatic
-// launch) and wait for it before they touch memory.
+// simply loses its top P and every entry's place on it is P_i - need_i.  The work is a scan over
+// at most 8192 entries and 8 bytes per page, and its time is the launch and four dependent trips
+// to memory: up to 128 entries one block of 128 threads (whose barriers cost half of 1024
+// threads': 64 decode steps with their slot map 5.7 us on the device), beyond a cluster of eight
+// blocks of 1024 that share the moving of the pages out (512 requests of up to 8192 tokens leave
+// and as many come, with their slot map: 16.1 us; one block 25.4).  The kernels here start while
+// their predecessor ends (programmatic launch) and wait for it before they touch memory.
 #include "paged.cuh"
 
 namespace fl {
@@ -83,19 +85,32 @@ template <int kT>
 struct Jobs {
   int32_t before[kT + 1], slot[kT], block0[kT];
 
-  template <class F>
-  __device__ void run(F&& move) const {
+  // thread `first` of `kAll`
+  template <int kAll, class F>
+  __device__ void run(int first, F&& move) const {
     const int n = before[kT];
-    for (int i0 = threadIdx.x; i0 < n; i0 += 4 * kT) {
+    for (int i0 = first; i0 < n; i0 += 4 * kAll) {
       int t[4];
 #pragma unroll
-      for (int y = 0; y < 4; ++y) t[y] = i0 + y * kT < n ? paged_find(before, kT, i0 + y * kT) : -1;
+      for (int y = 0; y < 4; ++y) t[y] = i0 + y * kAll < n ? paged_find(before, kT, i0 + y * kAll) : -1;
       move(t, i0);
     }
   }
 };
 
-template <int kT>
+// A cluster's CTAs all take the same steps over the entries; each moves its share of the pages,
+// and the first one alone writes what the others read (lengths, the count of free pages),
+// once all have read it.
+template <int kCtas>
+__device__ __forceinline__ void cluster_arrive() {
+  if constexpr (kCtas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+template <int kCtas>
+__device__ __forceinline__ void cluster_wait() {
+  if constexpr (kCtas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int kT, int kCtas>
 __global__ void __launch_bounds__(kT) extend_kernel(fl_paged_index x, int batch, const int32_t* slots,
                                                     const int32_t* n_new, int32_t* start, int32_t* cu) {
   extern __shared__ uint32_t s_bits[];
@@ -103,7 +118,9 @@ __global__ void __launch_bounds__(kT) extend_kernel(fl_paged_index x, int batch,
   __shared__ uint64_t red[kT / 32];
   __shared__ int s_taken;
   __shared__ Jobs<kT> jobs;
-  const int tid = threadIdx.x;
+  constexpr int kAll = kT * kCtas;
+  const int tid = threadIdx.x, rank = kCtas > 1 ? (int)blockIdx.x : 0;
+  const bool tell = rank == 0;
   Claims<kT> claims{s_bits, s_slot};
   claims.clear(x.slots);
   if (tid == 0) s_taken = 0;
@@ -116,19 +133,21 @@ __global__ void __launch_bounds__(kT) extend_kernel(fl_paged_index x, int batch,
     int s = -1, n = 0, c = 0, need = 0;
     if (b < batch) {
       n = n_new[b];
-      s = paged_slot(x, slots, b, true);
+      s = paged_slot(x, slots, b, tell);
       if (s >= 0) c = x.length[s];
     }
+    __syncwarp();
+    cluster_arrive<kCtas>();
     const bool named = s >= 0, mine = claims.first(s);
-    if (named && !mine) paged_error(x, FL_DEV_SLOT_TWICE, b);
+    if (named && !mine && tell) paged_error(x, FL_DEV_SLOT_TWICE, b);
     if (!mine) s = -1;
     if (s >= 0 && n < 0) {
-      paged_error(x, FL_DEV_COUNT, b);
+      if (tell) paged_error(x, FL_DEV_COUNT, b);
       s = -1;
     }
     if (s >= 0) {
       if (c < 0 || (int64_t)c + n > (int64_t)x.max_pages * FL_PAGE) {
-        paged_error(x, FL_DEV_TOO_LONG, b);
+        if (tell) paged_error(x, FL_DEV_TOO_LONG, b);
         s = -1;
       } else {
         need = ((c + n + FL_PAGE - 1) >> 6) - ((c + FL_PAGE - 1) >> 6);
@@ -138,18 +157,20 @@ __global__ void __launch_bounds__(kT) extend_kernel(fl_paged_index x, int batch,
     const uint64_t before = run + scan_pair<kT>((uint64_t)need << 32 | (uint32_t)max(n, 0), red, total);
     const int at = (int)(before >> 32);
     const bool granted = s >= 0 && (need == 0 || at + need <= n_free);
-    if (s >= 0 && !granted) paged_error(x, FL_DEV_NO_PAGE, b);
-    if (b < batch) {
+    if (s >= 0 && !granted && tell) paged_error(x, FL_DEV_NO_PAGE, b);
+    __syncwarp();
+    cluster_wait<kCtas>();
+    if (b < batch && tell) {
       start[b] = granted ? c : -1;
       cu[b] = (int)(uint32_t)before;
     }
-    if (granted) x.length[s] = c + n;
+    if (granted && tell) x.length[s] = c + n;
     const int count = granted ? need : 0;
     if (count > 0) atomicMax(&s_taken, at + count);
     const int block0 = (c + FL_PAGE - 1) >> 6;
     if (!__syncthreads_or(count > 1)) {
       // a decode step: a page a request at most
-      if (count == 1) x.table[(int64_t)s * x.max_pages + block0] = x.free_pages[n_free - 1 - at];
+      if (count == 1 && (tid >> 5) % kCtas == rank) x.table[(int64_t)s * x.max_pages + block0] = x.free_pages[n_free - 1 - at];
     } else {
       // the granted entries' pages lie one behind the other on the stack, from `base` on
       const int base = (int)(run >> 32), taken = max(s_taken - base, 0);
@@ -158,32 +179,34 @@ __global__ void __launch_bounds__(kT) extend_kernel(fl_paged_index x, int batch,
       jobs.block0[tid] = block0 - (at - base);
       if (tid == 0) jobs.before[kT] = taken;
       __syncthreads();
-      jobs.run([&](const int (&t)[4], int i0) {
+      jobs.template run<kAll>(rank * kT + tid, [&](const int (&t)[4], int i0) {
         int page[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) page[y] = t[y] >= 0 ? x.free_pages[n_free - 1 - base - (i0 + y * kT)] : 0;
+        for (int y = 0; y < 4; ++y) page[y] = t[y] >= 0 ? x.free_pages[n_free - 1 - base - (i0 + y * kAll)] : 0;
 #pragma unroll
         for (int y = 0; y < 4; ++y)
-          if (t[y] >= 0) x.table[(int64_t)jobs.slot[t[y]] * x.max_pages + jobs.block0[t[y]] + i0 + y * kT] = page[y];
+          if (t[y] >= 0) x.table[(int64_t)jobs.slot[t[y]] * x.max_pages + jobs.block0[t[y]] + i0 + y * kAll] = page[y];
       });
       __syncthreads();
     }
     run += total;
   }
   __syncthreads();
-  if (tid == 0) {
+  if (tid == 0 && tell) {
     cu[batch] = (int)(uint32_t)run;
     *x.n_free = n_free - s_taken;
   }
 }
 
-template <int kT>
+template <int kT, int kCtas>
 __global__ void __launch_bounds__(kT) release_kernel(fl_paged_index x, int batch, const int32_t* slots) {
   extern __shared__ uint32_t s_bits[];
   __shared__ int32_t s_slot[kT];
   __shared__ uint64_t red[kT / 32];
   __shared__ Jobs<kT> jobs;
-  const int tid = threadIdx.x;
+  constexpr int kAll = kT * kCtas;
+  const int tid = threadIdx.x, rank = kCtas > 1 ? (int)blockIdx.x : 0;
+  const bool tell = rank == 0;
   Claims<kT> claims{s_bits, s_slot};
   claims.clear(x.slots);
   grid_dep_launch();
@@ -192,33 +215,36 @@ __global__ void __launch_bounds__(kT) release_kernel(fl_paged_index x, int batch
   uint64_t given = 0;  // 2^27 at most
   for (int b0 = 0; b0 < batch; b0 += kT) {
     const int b = b0 + tid;
-    const int s = b < batch ? paged_slot(x, slots, b, true) : -1;
-    int count = s >= 0 ? (paged_length(x, s, b, true) + FL_PAGE - 1) >> 6 : 0;
+    const int s = b < batch ? paged_slot(x, slots, b, tell) : -1;
+    int count = s >= 0 ? (paged_length(x, s, b, tell) + FL_PAGE - 1) >> 6 : 0;
+    __syncwarp();
+    cluster_arrive<kCtas>();
     const bool mine = claims.first(s);
-    if (s >= 0 && !mine) paged_error(x, FL_DEV_SLOT_TWICE, b);
+    if (s >= 0 && !mine && tell) paged_error(x, FL_DEV_SLOT_TWICE, b);
     if (!mine) count = 0;
-    if (mine) x.length[s] = 0;
     uint64_t total;
     const int at = (int)scan_pair<kT>((uint64_t)count, red, total);
+    cluster_wait<kCtas>();
+    if (mine && tell) x.length[s] = 0;
     jobs.before[tid] = at;
     jobs.slot[tid] = s;
     jobs.block0[tid] = -at;
     if (tid == 0) jobs.before[kT] = (int)total;
     __syncthreads();
     const int64_t top = n_free + (int64_t)given;
-    jobs.run([&](const int (&t)[4], int i0) {
+    jobs.template run<kAll>(rank * kT + tid, [&](const int (&t)[4], int i0) {
       int page[4];
       int32_t* e[4];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         if (t[y] < 0) continue;
-        e[y] = x.table + (int64_t)jobs.slot[t[y]] * x.max_pages + jobs.block0[t[y]] + i0 + y * kT;
+        e[y] = x.table + (int64_t)jobs.slot[t[y]] * x.max_pages + jobs.block0[t[y]] + i0 + y * kAll;
         page[y] = *e[y];
       }
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         if (t[y] < 0) continue;
-        const int64_t to = top + i0 + y * kT;
+        const int64_t to = top + i0 + y * kAll;
         *e[y] = -1;
         // a stack that would grow beyond `pages` has been handed pages that are free already
         if (page[y] < 0 || page[y] >= x.pages || to >= x.pages) paged_error(x, FL_DEV_PAGE_RANGE, b0 + t[y]);
@@ -229,7 +255,7 @@ __global__ void __launch_bounds__(kT) release_kernel(fl_paged_index x, int batch
     given += total;
   }
   __syncthreads();
-  if (tid == 0) *x.n_free = (int)min((int64_t)n_free + (int64_t)given, (int64_t)x.pages);
+  if (tid == 0 && tell) *x.n_free = (int)min((int64_t)n_free + (int64_t)given, (int64_t)x.pages);
 }
 
 // Four consecutive rows a thread; the offsets are searched in shared memory where they fit.
@@ -300,6 +326,28 @@ __global__ void __launch_bounds__(kMapT) slot_map_kernel(fl_paged_index x, int b
   }
 }
 
+// Threads of the CTA for few entries, and threads and CTAs of the cluster for more.
+constexpr int kSmall = 128, kLarge = 1024, kCluster = 8;
+
+// launch_pdl of one cluster of `ctas`
+template <class... KArgs, class... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), int ctas, int threads, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
+}
+
 }  // namespace
 
 cudaError_t launch_paged_index_init(const fl_paged_index& x, cudaStream_t s) {
@@ -310,14 +358,15 @@ cudaError_t launch_paged_index_init(const fl_paged_index& x, cudaStream_t s) {
 cudaError_t launch_paged_extend(const fl_paged_index& x, int batch, const int32_t* slots, const int32_t* n_new,
                                 int32_t* start, int32_t* cu, cudaStream_t s) {
   const size_t bits = (size_t)(x.slots + 31) / 32 * 4;
-  if (batch <= 128) return launch_pdl(extend_kernel<128>, dim3(1), dim3(128), bits, s, x, batch, slots, n_new, start, cu);
-  return launch_pdl(extend_kernel<1024>, dim3(1), dim3(1024), bits, s, x, batch, slots, n_new, start, cu);
+  if (batch <= kSmall)
+    return launch_pdl(extend_kernel<kSmall, 1>, dim3(1), dim3(kSmall), bits, s, x, batch, slots, n_new, start, cu);
+  return launch_cluster(extend_kernel<kLarge, kCluster>, kCluster, kLarge, bits, s, x, batch, slots, n_new, start, cu);
 }
 
 cudaError_t launch_paged_release(const fl_paged_index& x, int batch, const int32_t* slots, cudaStream_t s) {
   const size_t bits = (size_t)(x.slots + 31) / 32 * 4;
-  if (batch <= 128) return launch_pdl(release_kernel<128>, dim3(1), dim3(128), bits, s, x, batch, slots);
-  return launch_pdl(release_kernel<1024>, dim3(1), dim3(1024), bits, s, x, batch, slots);
+  if (batch <= kSmall) return launch_pdl(release_kernel<kSmall, 1>, dim3(1), dim3(kSmall), bits, s, x, batch, slots);
+  return launch_cluster(release_kernel<kLarge, kCluster>, kCluster, kLarge, bits, s, x, batch, slots);
 }
 
 cudaError_t launch_paged_slot_map(const fl_paged_index& x, int batch, const int32_t* slots, const int32_t* start,
