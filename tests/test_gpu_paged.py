@@ -56,6 +56,29 @@ def test_tables_follow_the_oracle_through_random_steps(slots, max_pages, pages, 
     assert pair.c.status()[2] == 0
 
 
+def test_few_requests_of_many_pages():
+    r = np.random.default_rng(12)
+    slots, max_pages = 110, 210
+    pair = Pair(slots, max_pages, 9000, 1)
+    for step in range(5):
+        sl = r.permutation(slots)[:100]
+        sl[3], sl[60] = -1, sl[10]
+        n = r.integers(0, 64 * max_pages // 2, 100)
+        n[r.random(100) < 0.3] = 1
+        start, cu = pair.c.extend(i32(sl), i32(n))
+        ostart, ocu = pair.o.extend(sl, n)
+        assert start.tolist() == ostart.tolist() and cu.tolist() == ocu.tolist()
+        pair.same_index()
+        back = r.permutation(slots)[:50 + step]
+        back[7], back[20] = -1, back[9]
+        pair.c.release(i32(back))
+        pair.o.release(back, len(back))
+        pair.same_index()
+    code, detail, count = pair.c.status()
+    assert count == len(pair.o.errors) and (code, detail) in pair.o.errors
+    assert {c for c, _ in pair.o.errors} == {paged.FL_DEV_SLOT_TWICE, paged.FL_DEV_NO_PAGE}
+
+
 def test_one_long_request_and_an_empty_batch():
     pair = Pair(2, 16384, 16390, 1, max_batch=1)
     n = 16384 * 64
