@@ -7,13 +7,18 @@ namespace fl {
 namespace {
 
 // ---- append -----------------------------------------------------------------------------
-// A request whose blocks fill up is one item per such block and head; the item of the first one
-// also writes the head's new tail rows: that block is the only one whose older rows lie in the
-// tail, so the CTA has them in registers before it overwrites any.  A request that fills no
-// block (most of a decode step) is one item per 16 heads, a copy of its rows.
+// A request whose blocks fill up is two items per such block and head, keys and values (half the
+// registers of one item for both: 8 prompts of up to 4096 tokens, 16 heads, 71.7 -> 64.3 us with
+// their read-back); the items of the first one also write the head's new tail rows: that block is
+// the only one whose older rows lie in the tail, so the CTA has them in registers before it
+// overwrites any.  A request that fills no block (most of a decode step) is one item per 16 heads,
+// a copy of its rows.  Bound by instructions (20 a value) and the two barriers of a key item: those
+// prompts' 105 MB in 37 us, 2.9 TB/s.  Four CTAs an SM: 64.3 us with the read-back, three 69.9,
+// five 65.4, six 66.8, and a CTA per item 68.8.  The division alone, per word of eight codes with
+// one near a half, instead of per code: 63.7 instead of 58.6.
 //
-// 256 threads: thread t owns channels 8 (t % 16) .. + 7 of rows t / 16 + 16 i, i = 0..3, of
-// keys and values (16-byte loads, 256-byte rows).  A value group (row, 64-channel half) is
+// 256 threads: thread t owns channels 8 (t % 16) .. + 7 of rows t / 16 + 16 i, i = 0..3
+// (16-byte loads, 256-byte rows).  A value group (row, 64-channel half) is
 // eight neighbouring threads: three steps of shuffles, after which each pair of threads has one
 // of the four rows and computes its scale and zero for all eight.  A key group (channel) is 64 rows: four in the
 // thread, two row sets in the warp, eight warps through shared memory.  Minima and maxima are
@@ -35,16 +40,16 @@ __device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
-// Eight codes by quant() of quant.cuh; one copy of the code, for the rare call below.
-__device__ __noinline__ uint32_t quant_word_exact(uint4 x, uint4 sz0, uint4 sz1) {
-  const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, sz[8] = {sz0.x, sz0.y, sz0.z, sz0.w, sz1.x, sz1.y, sz1.z, sz1.w};
-  uint32_t w = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float2 f = unpack_sz(sz[e]);
-    w |= quant(e & 1 ? bf16_hi(xs[e >> 1]) : bf16_lo(xs[e >> 1]), f.x, f.y) << (4 * e);
-  }
-  return w;
+__device__ __forceinline__ float rcp_approx(float s) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+// One code by quant() of quant.cuh; one copy of the code, for the rare call below.
+__device__ __noinline__ uint32_t quant_exact(uint16_t x, uint32_t sz) {
+  const float2 f = unpack_sz(sz);
+  return quant(__uint_as_float((uint32_t)x << 16), f.x, f.y);
 }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -71,28 +76,38 @@ __device__ __forceinline__ float mul_sat(float a, float b) {
   return d;
 }
 
-// The same with the rounded division taken only near a half.  u = (x - z) r / 15, cut off to
-// [0, 1], with r / 15 to 2^-22, so 15 u is d / s to 1e-5 for codes up to 16 (beyond, both clamp),
-// and the rounded quotient is within 2^-20 of d / s: away from a half by 1e-4 all of them round
-// to the same code.  Cutting off is free in the product, and gives 0 for the NaN of an infinity,
-// as there.  Rounding is an addition of 1.5 2^23, after which four codes add up to 16 bits
-// exactly: no conversions, which issue at a quarter of the rate, and no shifts.
-// nz = -z of the channel pairs, r15 = r / 15; `close`: a code is to be taken from
-// quant_word_exact.
-__device__ __forceinline__ uint32_t quant_word(uint4 x, const float2* nz, const float2* r15, bool& close) {
-  constexpr float kMagic = 12582912.f;
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Eight codes, with the rounded division taken only near a half.  u = (x - z) r / 15, cut off to
+// [0, 1], with r / 15 to 2^-22 and the product to 2^-24: 15 u is d / s to 4.8e-6 for codes up to 16
+// (beyond, both clamp), and the rounded quotient is within 1e-6 of d / s, so away from a half by
+// 1e-5 all of them round to the same code.  Not so rare: BF16 values and binary16 scales are
+// coarse, and 7 of 10,000 normal values are exact halves.
+// Cutting off is free in the product, and gives 0 for the NaN of an infinity, as quant() does.
+// Rounding is an addition of 1.5 2^23, after which four codes add up to 16 bits exactly: no
+// conversions, which issue at a quarter of the rate, and no shifts.  nz = -z of the channel
+// pairs, r15 = r / 15; row: the values in memory, sz(e): scale and zero of value e.
+template <class F>
+__device__ __forceinline__ uint32_t quant_word(uint4 x, const float2* nz, const float2* r15, const uint16_t* row,
+                                               F&& sz) {
+  constexpr float kMagic = 12582912.f, kNear = 0.49999f;
   const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-  const float2 c15 = make_float2(15.f, 15.f), magic = make_float2(kMagic, kMagic), back = make_float2(-kMagic, -kMagic);
+  const float2 c15 = make_float2(15.f, 15.f), cm15 = make_float2(-15.f, -15.f), magic = make_float2(kMagic, kMagic),
+               back = make_float2(-kMagic, -kMagic);
   float worst = 0.f;
-  float2 code[4], up[4];
+  float2 code[4], up[4], off[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float2 d = add2(make_float2(bf16_lo(xs[e]), bf16_hi(xs[e])), nz[e]);
     const float2 u = make_float2(mul_sat(d.x, r15[e].x), mul_sat(d.y, r15[e].y));
     up[e] = fma2(u, c15, magic);
     code[e] = add2(up[e], back);
-    const float2 off = fma2(u, c15, make_float2(-code[e].x, -code[e].y));
-    worst = fmaxf(worst, fmaxf(fabsf(off.x), fabsf(off.y)));
+    off[e] = fma2(u, cm15, code[e]);
+    worst = max_abs3(worst, off[e].x, off[e].y);
   }
   uint32_t half[2];
 #pragma unroll
@@ -101,16 +116,23 @@ __device__ __forceinline__ uint32_t quant_word(uint4 x, const float2* nz, const 
     const float2 two = fma2(code[2 * i + 1], c256, make_float2(up[2 * i].x, code[2 * i].y));
     half[i] = __float_as_uint(fmaf(two.y, 16.f, two.x));
   }
-  close = worst >= 0.4999f;
-  return __byte_perm(half[0], half[1], 0x5410);
+  uint32_t w = __byte_perm(half[0], half[1], 0x5410);
+  if (worst >= kNear) {
+    unsigned near = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      near |= (unsigned)(fabsf(off[e].x) >= kNear) << (2 * e) | (unsigned)(fabsf(off[e].y) >= kNear) << (2 * e + 1);
+#pragma unroll 1
+    for (; near; near &= near - 1) {
+      const int e = __ffs(near) - 1;
+      w = (w & ~(15u << (4 * e))) | quant_exact(row[e], sz(e)) << (4 * e);
+    }
+  }
+  return w;
 }
 
 // 1 / (15 s) to 2^-22, and 0 for s = 0 (whose code is 0); binary16 scales are at least 2^-24.
-__device__ __forceinline__ float rcp_scale(float s) {
-  float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
-  return s == 0.f ? 0.f : r * (1.f / 15.f);
-}
+__device__ __forceinline__ float rcp_scale(float s) { return s == 0.f ? 0.f : rcp_approx(s) * (1.f / 15.f); }
 
 __global__ void __launch_bounds__(kAT, kAppendCtas) append_kernel(PagedAppendArgs a) {
   extern __shared__ int32_t prefix[];
@@ -159,20 +181,21 @@ __global__ void __launch_bounds__(kAT, kAppendCtas) append_kernel(PagedAppendArg
     uint16_t* tail = (values ? a.p.tail_v : a.p.tail_k) + ((size_t)s * heads + h) * FL_PAGE * kD + 8 * chunk;
     const uint16_t* rows = (values ? a.v : a.k) + (int64_t)(row0 - c) * a.token_stride + (int64_t)h * a.head_stride + 8 * chunk;
     const int page = x.table[(int64_t)s * x.max_pages + block];
+    const int64_t step = 16 * a.token_stride;
+    const int t0 = block * FL_PAGE + r0;
+    const uint16_t *old = tail + r0 * kD, *row_t0 = rows + t0 * a.token_stride;
     auto from = [&](int i) {
-      const int row = r0 + 16 * i, t = block * FL_PAGE + row;
-      return reinterpret_cast<const uint4*>(t < c ? tail + row * kD : rows + t * a.token_stride);
+      return t0 + 16 * i < c ? old + 16 * i * kD : row_t0 + i * step;
     };
     uint4 x4[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x4[i] = *from(i);
+    for (int i = 0; i < 4; ++i) x4[i] = *reinterpret_cast<const uint4*>(from(i));
     const bool paged = page >= 0 && page < x.pages;
     if (!paged && tid == 0) paged_error(x, FL_DEV_PAGE_RANGE, b);
     uint8_t* rec = a.p.rec + ((size_t)(paged ? page : 0) * heads + h) * kRec;
     auto code_at = [&](int i) {
       return reinterpret_cast<uint32_t*>(rec + (r0 + 16 * i) * 128 + (values ? 64 : 0) + 4 * chunk);
     };
-    unsigned again = 0;
     if (paged && !values) {
       // keys: this thread's four rows, the warp's other row set, then the eight warps
       uint32_t mn[4], mx[4];
@@ -216,17 +239,7 @@ __global__ void __launch_bounds__(kAT, kAppendCtas) append_kernel(PagedAppendArg
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-        {
-          bool close;
-          *code_at(i) = quant_word(x4[i], nz, r15, close);
-          again |= (unsigned)close << i;
-        }
-      }
-      while (again) {
-        const int i = __ffs(again) - 1;
-        again &= again - 1;
-        *code_at(i) = quant_word_exact(*from(i), *reinterpret_cast<const uint4*>(&sm.sz[8 * chunk]),
-                                       *reinterpret_cast<const uint4*>(&sm.sz[8 * chunk + 4]));
+          *code_at(i) = quant_word(x4[i], nz, r15, from(i), [&](int e) { return sm.sz[8 * chunk + e]; });
       }
     } else if (paged) {
       // values: each step of the reduction halves the rows a thread still answers for
@@ -264,26 +277,16 @@ __global__ void __launch_bounds__(kAT, kAppendCtas) append_kernel(PagedAppendArg
         const float rv = rcp_scale(f.x);
         const float2 z2 = make_float2(-f.y, -f.y), r2 = make_float2(rv, rv);
         const float2 nz[4] = {z2, z2, z2, z2}, r15[4] = {r2, r2, r2, r2};
-        bool close;
-        *code_at(i) = quant_word(x4[i], nz, r15, close);
-        again |= (unsigned)close << i;
-      }
-      if (__any_sync(kFull, again != 0)) {
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t both = __shfl_sync(kFull, mine, (lane & 24) + 2 * i);
-          const uint4 sz = make_uint4(both, both, both, both);
-          if (again >> i & 1) *code_at(i) = quant_word_exact(*from(i), sz, sz);
-        }
+        *code_at(i) = quant_word(x4[i], nz, r15, from(i), [&](int) { return both; });
       }
     }
     if (j == 0) {
       __syncthreads();  // every old tail row is in registers
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = r0 + 16 * i, t = full1 * FL_PAGE + row;
+        const int t = full1 * FL_PAGE + r0 + 16 * i;
         if (t >= c && t < n)
-          *reinterpret_cast<uint4*>(tail + row * kD) = *reinterpret_cast<const uint4*>(rows + t * a.token_stride);
+          *reinterpret_cast<uint4*>(tail + (r0 + 16 * i) * kD) = *reinterpret_cast<const uint4*>(rows + t * a.token_stride);
       }
     }
   }
