@@ -140,7 +140,8 @@ fl_status fl_paged_append(const fl_paged_index* index, const fl_paged_pool* pool
   if ((st = check_batch(index, batch, slots)) != FL_OK) return st;
   if (n_tokens < 0) return FL_ERR_INVALID;
   if (batch == 0 || n_tokens == 0) return FL_OK;
-  if (((int64_t)batch + n_tokens / FL_PAGE) * pool->kv_heads > INT32_MAX) return FL_ERR_UNSUPPORTED;  // work items
+  // work items are counted in 32 bits, with room for one more step of the grid
+  if (2 * ((int64_t)batch + n_tokens / FL_PAGE) * pool->kv_heads > INT32_MAX - 65536) return FL_ERR_UNSUPPORTED;
   if (!start || !cu || !aligned(start, 4) || !aligned(cu, 4)) return FL_ERR_INVALID;
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !good_strides(token_stride, head_stride, 8))
     return FL_ERR_INVALID;

@@ -391,7 +391,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
   if (a.batch == 0 || a.n_tokens == 0) return cudaSuccess;
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  // at most one item per entry and one more per 64 tokens
+  // at most two items per entry, two more per 64 tokens
   const int64_t items = 2 * ((int64_t)a.batch + a.n_tokens / FL_PAGE) * a.p.kv_heads;
   const int grid = (int)(items < kAppendCtas * sms ? items : kAppendCtas * sms);
   return launch_pdl(append_kernel, dim3(grid), dim3(kAT), (size_t)(a.batch + 1) * 4, s, a);

@@ -123,6 +123,16 @@ def test_append_and_read_check_their_arguments():
     assert rd(t=0) == abi.FL_OK
 
 
+def test_append_refuses_more_work_than_it_counts():
+    # two items per entry and per 64 tokens, for each head, in 32 bits
+    x, p = index(), pool(kv_heads=32)
+    app = lambda t: paged._c_append(ref(x), ref(p), 1, None, FAKE, FAKE, t, FAKE, FAKE + 8, 4096, 128, None)  # noqa: E731
+    most = (2 ** 31 - 1 - 65536) // 64 - 1
+    assert app(most * 64 + 63) == abi.FL_ERR_INVALID            # v is not aligned: the count itself passed
+    assert app((most + 1) * 64) == abi.FL_ERR_UNSUPPORTED
+    assert app(2 ** 31 - 1) == abi.FL_ERR_UNSUPPORTED
+
+
 def test_attention_and_selection_check_their_arguments():
     x, p = index(), pool()
     ws = paged._c_ws_bytes(ref(x), ref(p), 3, 4)
