@@ -10,9 +10,9 @@
 // to memory.  Up to 128 entries of not too many pages one block of 128 threads does it (whose
 // barriers cost half of 1024 threads': 64 decode steps with their slot map 5.7 us on the device),
 // else a cluster of eight blocks that share the moving of the pages out (512 requests of up to
-// 8192 tokens leave and as many come, with their slot map: 16.1 us; one block of 1024 threads
-// 25.4).  The kernels here start while their predecessor ends (programmatic launch) and wait for
-// it before they touch memory.
+// 8192 tokens leave and as many come, with their slot map: 14.4 us in blocks of 512 threads, 16.4
+// of 1024, 19.4 of 256; one block of 1024 threads 25.4).  The kernels here start while their
+// predecessor ends (programmatic launch) and wait for it before they touch memory.
 #include "paged.cuh"
 
 namespace fl {
@@ -328,10 +328,10 @@ __global__ void __launch_bounds__(kMapT) slot_map_kernel(fl_paged_index x, int b
 }
 
 // Threads of a CTA for few entries and for more, and CTAs of the cluster.
-constexpr int kSmall = 128, kLarge = 1024, kCluster = 8;
+constexpr int kSmall = 128, kLarge = 512, kCluster = 8;
 // Few entries take the cluster where they could have more pages than this.  It costs an extend
-// and a release 0.65 us each (64 requests, one token: 4.0 us together, 5.2 as clusters) and saves
-// 43 us for 64 x 8192 tokens (54.6, 11.4) and 354 for 128 x 32768 (411.9, 58.1).  An extend is
+// and a release 1 us each (64 requests, one token: 3.9 us together, 5.9 as clusters) and saves
+// 50 us for 128 x 8192 tokens (60.5, 10.0) and 390 for 128 x 32768 (412, 22.9).  An extend is
 // called for every token, mostly without a page to move; a release once a request.
 constexpr int kExtendPages = 16384, kReleasePages = 256;
 
@@ -364,18 +364,15 @@ cudaError_t launch_paged_index_init(const fl_paged_index& x, cudaStream_t s) {
 cudaError_t launch_paged_extend(const fl_paged_index& x, int batch, const int32_t* slots, const int32_t* n_new,
                                 int32_t* start, int32_t* cu, cudaStream_t s) {
   const size_t bits = (size_t)(x.slots + 31) / 32 * 4;
-  if (batch <= kSmall && (int64_t)batch * x.max_pages > kExtendPages)
-    return launch_cluster(extend_kernel<kSmall, kCluster>, kCluster, kSmall, bits, s, x, batch, slots, n_new, start, cu);
-  if (batch <= kSmall)
+  if (batch <= kSmall && (int64_t)batch * x.max_pages <= kExtendPages)
     return launch_pdl(extend_kernel<kSmall, 1>, dim3(1), dim3(kSmall), bits, s, x, batch, slots, n_new, start, cu);
   return launch_cluster(extend_kernel<kLarge, kCluster>, kCluster, kLarge, bits, s, x, batch, slots, n_new, start, cu);
 }
 
 cudaError_t launch_paged_release(const fl_paged_index& x, int batch, const int32_t* slots, cudaStream_t s) {
   const size_t bits = (size_t)(x.slots + 31) / 32 * 4;
-  if (batch <= kSmall && (int64_t)batch * x.max_pages > kReleasePages)
-    return launch_cluster(release_kernel<kSmall, kCluster>, kCluster, kSmall, bits, s, x, batch, slots);
-  if (batch <= kSmall) return launch_pdl(release_kernel<kSmall, 1>, dim3(1), dim3(kSmall), bits, s, x, batch, slots);
+  if (batch <= kSmall && (int64_t)batch * x.max_pages <= kReleasePages)
+    return launch_pdl(release_kernel<kSmall, 1>, dim3(1), dim3(kSmall), bits, s, x, batch, slots);
   return launch_cluster(release_kernel<kLarge, kCluster>, kCluster, kLarge, bits, s, x, batch, slots);
 }
 
