@@ -184,6 +184,44 @@ def test_codes_at_every_half_are_the_rounded_divisions():
     pair.same_bytes()
 
 
+def near_half_groups(r, n):
+    """BF16 values [n][64] whose quotients (x - z) / s lie at, and a few units in the last place
+    beside, halves: among them groups with z = -(a + 0.5) s, where tiny values do."""
+    s = np.exp2(r.integers(-18, 9, (n, 1))) * (1 + r.integers(0, 8, (n, 1)) / 8)
+    z = -(r.integers(0, 15, (n, 1)) + r.choice([0.0, 0.5], (n, 1))) * s * r.choice([1, 1, 1, 0, 40], (n, 1))
+    x = torch.from_numpy(z + (r.integers(0, 15, (n, 64)) + 0.5) * s).bfloat16()
+    x = (x.view(torch.int16) + torch.from_numpy(r.integers(-2, 3, (n, 64))).short()).view(torch.bfloat16)
+    tiny = torch.from_numpy(r.choice([0.0, -0.0, 1e-40, -1e-40, 1e-30, -1e-30, 1e-8, -1e-8], (n, 64))).bfloat16()
+    x = torch.where(torch.from_numpy(r.random((n, 64)) < 0.3), tiny, x)
+    x[:, 0], x[:, 63] = torch.from_numpy(z[:, 0]).bfloat16(), torch.from_numpy(z[:, 0] + 15 * s[:, 0]).bfloat16()
+    x = torch.where(x.isfinite(), x, 0.0)
+    x[::97] -= 66560.0                           # zero beyond the 16-bit numbers, a finite scale
+    return x
+
+
+def test_codes_beside_halves_are_the_rounded_divisions():
+    r = np.random.default_rng(31)
+    m = 120
+    pair = Pair(1, m + 1, m + 1, 1)
+    k = near_half_groups(r, m * D).reshape(m, D, 64).transpose(1, 2).reshape(m * 64, 1, D)
+    v = near_half_groups(r, m * 64 * 2).reshape(m * 64, 1, D)
+    k, v = (torch.cat([t, torch.zeros(1, 1, D, dtype=torch.bfloat16)]).contiguous() for t in (k, v))
+    start, cu = pair.c.extend(i32([0]), i32([len(k)]))
+    pair.c.append(0, i32([0]), start, cu, k.cuda(), v.cuda())
+    s, c = pair.o.extend([0], [len(k)])
+    pair.o.append([0], s, c, f32(k), f32(v))
+
+    def plain(rec):
+        # the least of a group that holds both zeros is either of them: -0 as 0 in the scale words
+        sz = rec[..., 8192:].view(np.uint16)
+        sz[sz == 0x8000] = 0
+        return rec
+
+    got, want = plain(pair.c.pools[0].rec.cpu().numpy()), plain(pair.o.rec.copy())
+    for j in range(m):
+        assert np.array_equal(got[pair.o.table[0, j]], want[pair.o.table[0, j]]), j
+
+
 def test_append_skips_rows_beyond_its_input_and_bad_pages():
     g = gen(6)
     pair = Pair(3, 4, 9, 1)
