@@ -12,10 +12,11 @@ namespace {
 // their read-back); the items of the first one also write the head's new tail rows: that block is
 // the only one whose older rows lie in the tail, so the CTA has them in registers before it
 // overwrites any.  A request that fills no block (most of a decode step) is one item per 16 heads,
-// a copy of its rows.  Bound by instructions (20 a value) and the two barriers of a key item: those
-// prompts' 105 MB in 37 us, 2.9 TB/s.  Four CTAs an SM: 64.3 us with the read-back, three 69.9,
-// five 65.4, six 66.8, and a CTA per item 68.8.  The division alone, per word of eight codes with
-// one near a half, instead of per code: 63.7 instead of 58.6.
+// a copy of its rows.  Bound by instructions (19 a value) and the two barriers of a key item: those
+// prompts' 105 MB in 34 us, 3.1 TB/s, 55.6 with the read-back.  Four CTAs an SM: 64.3 us with the
+// read-back before the last steps, three 69.9, five 65.4, six 66.8, and a CTA per item 68.8.
+// The division per word of eight codes with one near a half instead of per code: 63.7 for 58.6;
+// each thread's own reciprocals of its channels' scales instead of one per channel: 58.6 for 55.6.
 //
 // 256 threads: thread t owns channels 8 (t % 16) .. + 7 of rows t / 16 + 16 i, i = 0..3
 // (16-byte loads, 256-byte rows).  A value group (row, 64-channel half) is
@@ -25,9 +26,10 @@ namespace {
 // taken on the BF16 values, exact.
 constexpr int kAT = 256, kAppendCtas = 4;
 
-struct AppendSmem {
+struct alignas(16) AppendSmem {
   uint32_t mn[8][64], mx[8][64];  // per warp and channel pair
-  uint32_t sz[kD];
+  uint32_t sz[kD];                // of each channel: scale and zero, -z, 1 / (15 s)
+  float nz[kD], r15[kD];
   int red[kAT / 32];
 };
 
@@ -223,19 +225,19 @@ __global__ void __launch_bounds__(kAT, kAppendCtas) append_kernel(PagedAppendArg
         __half hs, hz;
         group_sz(__uint_as_float((lo >> sh) << 16), __uint_as_float((hi >> sh) << 16), hs, hz);
         sm.sz[tid] = pack_sz(hs, hz);
+        sm.nz[tid] = -__half2float(hz);
+        sm.r15[tid] = rcp_scale(__half2float(hs));
         reinterpret_cast<uint32_t*>(rec + kRecKsz)[tid] = pack_sz(hs, hz);
       }
       __syncthreads();
       {
-        const uint4 s0 = *reinterpret_cast<const uint4*>(&sm.sz[8 * chunk]);
-        const uint4 s1 = *reinterpret_cast<const uint4*>(&sm.sz[8 * chunk + 4]);
-        const uint32_t w[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
         float2 nz[4], r15[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 a0 = unpack_sz(w[2 * e]), a1 = unpack_sz(w[2 * e + 1]);
-          nz[e] = make_float2(-a0.y, -a1.y);
-          r15[e] = make_float2(rcp_scale(a0.x), rcp_scale(a1.x));
+        for (int e = 0; e < 4; e += 2) {
+          const float4 z4 = *reinterpret_cast<const float4*>(&sm.nz[8 * chunk + 2 * e]);
+          const float4 r4 = *reinterpret_cast<const float4*>(&sm.r15[8 * chunk + 2 * e]);
+          nz[e] = make_float2(z4.x, z4.y), nz[e + 1] = make_float2(z4.z, z4.w);
+          r15[e] = make_float2(r4.x, r4.y), r15[e + 1] = make_float2(r4.z, r4.w);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
