@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kAT, kAppendCtas) append_kernel(PagedAppendArg
 #pragma unroll
     for (int i = 0; i < 4; ++i) x4[i] = *reinterpret_cast<const uint4*>(from(i));
     const bool paged = page >= 0 && page < x.pages;
-    if (!paged && tid == 0) paged_error(x, FL_DEV_PAGE_RANGE, b);
+    if (!paged && !values && tid == 0) paged_error(x, FL_DEV_PAGE_RANGE, b);  // once a block and head
     uint8_t* rec = a.p.rec + ((size_t)(paged ? page : 0) * heads + h) * kRec;
     auto code_at = [&](int i) {
       return reinterpret_cast<uint32_t*>(rec + (r0 + 16 * i) * 128 + (values ? 64 : 0) + 4 * chunk);

@@ -241,6 +241,16 @@ def test_append_skips_rows_beyond_its_input_and_bad_pages():
     assert pair.c.status()[0] == paged.FL_DEV_PAGE_RANGE and not out.any()
 
 
+def test_a_bad_page_is_told_once_a_block_and_head():
+    pair = Pair(2, 3, 6, 3)
+    start, cu = pair.c.extend(i32([1, 0]), i32([10, 129]))
+    pair.c.index.table[0, 1] = 6
+    k = bf16(gen(8), 139, 3, D).cuda()
+    pair.c.append(0, i32([1, 0]), start, cu, k, k)
+    assert pair.c.status() == [paged.FL_DEV_PAGE_RANGE, 1, 3]
+    assert torch.equal(pair.c.pools[0].tail_v[0, :, 0], k[138])
+
+
 # ------------------------------------------------------------------------------- attention
 LENGTHS = [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 300, 1000, 1345]
 
