@@ -308,9 +308,10 @@ __device__ __forceinline__ uint32_t bf2(float a, float b) {
   __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&r);
 }
-// nibble e of w as an exact float
-__device__ __forceinline__ float nib(uint32_t w, int e) {
-  return __uint_as_float(((w >> (4 * e)) & 15u) | 0x4B000000u) - 8388608.f;
+// Byte e of x, below 2^4, as an exact float: under the exponent of 2^23 it is 2^23 + x
+template <int e>
+__device__ __forceinline__ float low_byte(uint32_t x) {
+  return __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7550 + e)) - 8388608.f;
 }
 
 __global__ void __launch_bounds__(kReadWarps * 32, kReadCtas) read_kernel(PagedReadArgs a) {
@@ -336,11 +337,15 @@ __global__ void __launch_bounds__(kReadWarps * 32, kReadCtas) read_kernel(PagedR
   auto put = [&](int r, uint32_t kw, uint32_t vw, uint32_t vz) {
     const float2 vsz = unpack_sz(vz);
     uint4 ko, vo;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      (&ko.x)[e] = bf2(fmaf(nib(kw, 2 * e), ksz[2 * e].x, ksz[2 * e].y), fmaf(nib(kw, 2 * e + 1), ksz[2 * e + 1].x, ksz[2 * e + 1].y));
-      (&vo.x)[e] = bf2(fmaf(nib(vw, 2 * e), vsz.x, vsz.y), fmaf(nib(vw, 2 * e + 1), vsz.x, vsz.y));
-    }
+    const uint32_t k0 = kw & 0x0f0f0f0fu, k1 = kw >> 4 & 0x0f0f0f0fu, v0 = vw & 0x0f0f0f0fu, v1 = vw >> 4 & 0x0f0f0f0fu;
+    ko.x = bf2(fmaf(low_byte<0>(k0), ksz[0].x, ksz[0].y), fmaf(low_byte<0>(k1), ksz[1].x, ksz[1].y));
+    ko.y = bf2(fmaf(low_byte<1>(k0), ksz[2].x, ksz[2].y), fmaf(low_byte<1>(k1), ksz[3].x, ksz[3].y));
+    ko.z = bf2(fmaf(low_byte<2>(k0), ksz[4].x, ksz[4].y), fmaf(low_byte<2>(k1), ksz[5].x, ksz[5].y));
+    ko.w = bf2(fmaf(low_byte<3>(k0), ksz[6].x, ksz[6].y), fmaf(low_byte<3>(k1), ksz[7].x, ksz[7].y));
+    vo.x = bf2(fmaf(low_byte<0>(v0), vsz.x, vsz.y), fmaf(low_byte<0>(v1), vsz.x, vsz.y));
+    vo.y = bf2(fmaf(low_byte<1>(v0), vsz.x, vsz.y), fmaf(low_byte<1>(v1), vsz.x, vsz.y));
+    vo.z = bf2(fmaf(low_byte<2>(v0), vsz.x, vsz.y), fmaf(low_byte<2>(v1), vsz.x, vsz.y));
+    vo.w = bf2(fmaf(low_byte<3>(v0), vsz.x, vsz.y), fmaf(low_byte<3>(v1), vsz.x, vsz.y));
     __stcs(reinterpret_cast<uint4*>(a.k + out + r * a.token_stride), ko);
     __stcs(reinterpret_cast<uint4*>(a.v + out + r * a.token_stride), vo);
   };
