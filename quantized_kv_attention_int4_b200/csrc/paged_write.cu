@@ -298,10 +298,10 @@ __global__ void __launch_bounds__(kAT, kAppendCtas) append_kernel(PagedAppendArg
 // One warp takes 8 consecutive rows of one head: lane l owns channels 8 (l % 16) .. + 7 of
 // rows l / 16, l / 16 + 2, ....  Rows of one page in order, the usual case, are read all at once;
 // otherwise one after the other, the key scales staying in registers while the page does not
-// change.  Bound by memory at length (6 requests of up to 32768 tokens, 8 heads: 504 MB in 87 us,
-// 5.8 TB/s), by one trip to it when short.  16 rows a warp, in two goes of loads: 13.6 us for
-// 4096 tokens of 16 heads instead of 10.8.  Eight warps a CTA 93 us, four 90, and 87 with nine
-// of these an SM (56 registers; ten 91).
+// change.  Bound by memory at length (6 requests of up to 32768 tokens, 8 heads: 504 MB in 86 us,
+// 5.9 TB/s), by one trip to it when short.  16 rows a warp, in two goes of loads: 13.6 us for
+// 4096 tokens of 16 heads instead of 10.8.  Eight warps a CTA 93 us, four 90, 88 with nine of
+// these an SM (56 registers; ten 91), 86 with nibbles taken by byte; packed arithmetic 87.
 constexpr int kReadRows = 8, kReadWarps = 4, kReadCtas = 9;
 
 __device__ __forceinline__ uint32_t bf2(float a, float b) {
