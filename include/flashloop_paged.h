@@ -60,7 +60,7 @@ extern "C" {
 #define FL_DEV_SLOT_TWICE 17   /* a slot named twice in a call that changes it: the first entry counts */
 #define FL_DEV_NO_PAGE 18      /* not enough free pages: the request is left as it was */
 #define FL_DEV_TOO_LONG 19     /* a length outside [0, 64 max_pages], or growth beyond it */
-#define FL_DEV_COUNT 20        /* a negative token count, or offsets that do not ascend or pass n_tokens */
+#define FL_DEV_COUNT 20        /* a negative token count, more than 2^31 - 1 rows, or offsets that do not ascend or pass n_tokens */
 #define FL_DEV_PAGE_RANGE 21   /* a page, or a place of a slot map, outside the pool: skipped */
 #define FL_DEV_SEL_BLOCK 22    /* a selected block that is no full block of its request: skipped */
 
@@ -93,8 +93,8 @@ fl_status fl_paged_index_init(const fl_paged_index* index, void* stream);
  * 64 max_pages tokens, or too few pages: an entry that needs pages is refused once the
  * pages needed by the valid entries up to it exceed the free ones; a refused request is left
  * as it was).  cu [batch + 1] receives the offsets of the entries' rows in the packed input:
- * cu[0] = 0, cu[i + 1] = cu[i] + max(n_new[i], 0), whether or not entry i is refused.  The
- * total must stay below 2^31. */
+ * cu[0] = 0, cu[i + 1] = cu[i] + max(n_new[i], 0), whether or not entry i is refused, but at
+ * most 2^31 - 1: an entry with rows beyond that is refused too (FL_DEV_COUNT). */
 fl_status fl_paged_extend(const fl_paged_index* index, int32_t batch, const int32_t* slots, const int32_t* n_new,
                           int32_t* start, int32_t* cu, void* stream);
 

@@ -73,7 +73,8 @@ class PagedOracle:
     def extend(self, slots, n_new):
         start, cu, seen, wanted, n_free = [], [0], set(), 0, len(self.free)
         for b, n in enumerate(int(n) for n in n_new):
-            cu.append(cu[-1] + max(n, 0))
+            rows = cu[-1] + max(n, 0)
+            cu.append(min(rows, 2 ** 31 - 1))
             s = self._named(slots, b, seen)
             start.append(-1)
             if s < 0:
@@ -84,6 +85,9 @@ class PagedOracle:
                 continue
             if c + n > self.max_pages * PAGE:
                 self.errors.append((TOO_LONG, b))
+                continue
+            if n and rows > 2 ** 31 - 1:
+                self.errors.append((COUNT, b))
                 continue
             need = blocks(c + n) - blocks(c)
             wanted += need

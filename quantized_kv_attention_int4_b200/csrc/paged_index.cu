@@ -56,9 +56,15 @@ struct Claims {
   }
 };
 
-// Two sums at once: `v`'s halves (below 2^32 each in total).
+// A chunk's tokens and pages are summed in one number, pages from this bit on: 512 entries of less
+// than 2^31 tokens, refused ones among them, stay below it, and their 2^14 pages each in the rest.
+constexpr int kPageBit = 40, kChunkMost = 512;
+constexpr uint64_t kTokens = ((uint64_t)1 << kPageBit) - 1;
+
+// Exclusive prefix sum of one such number per thread.
 template <int kT>
 __device__ __forceinline__ uint64_t scan_pair(uint64_t v, uint64_t* red, uint64_t& total) {
+  static_assert(kT <= kChunkMost, "a chunk's tokens would reach its pages");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint64_t x = v;
 #pragma unroll
@@ -128,7 +134,8 @@ __global__ void __launch_bounds__(kT) extend_kernel(fl_paged_index x, int batch,
   grid_dep_launch();
   grid_dep_wait();
   const int n_free = min(max(*x.n_free, 0), x.pages);
-  uint64_t run = 0;  // tokens, and pages needed in the high half (2^27 at most)
+  int64_t rows = 0;  // of the chunks before
+  int base = 0;      // pages that they need (2^27 at most)
   for (int b0 = 0; b0 < batch; b0 += kT) {
     const int b = b0 + tid;
     int s = -1, n = 0, c = 0, need = 0;
@@ -155,15 +162,19 @@ __global__ void __launch_bounds__(kT) extend_kernel(fl_paged_index x, int batch,
       }
     }
     uint64_t total;
-    const uint64_t before = run + scan_pair<kT>((uint64_t)need << 32 | (uint32_t)max(n, 0), red, total);
-    const int at = (int)(before >> 32);
-    const bool granted = s >= 0 && (need == 0 || at + need <= n_free);
-    if (s >= 0 && !granted && tell) paged_error(x, FL_DEV_NO_PAGE, b);
+    const uint64_t before = scan_pair<kT>((uint64_t)need << kPageBit | (uint32_t)max(n, 0), red, total);
+    const int at = base + (int)(before >> kPageBit);
+    const int64_t row0 = rows + (int64_t)(before & kTokens);
+    // rows that offsets cannot name: this entry is refused, and so is all behind it that has rows
+    // (so that the pages it would have needed hold up none that is granted)
+    const bool counted = n <= 0 || row0 + n <= INT32_MAX;
+    const bool granted = s >= 0 && counted && (need == 0 || at + need <= n_free);
+    if (s >= 0 && !granted && tell) paged_error(x, counted ? FL_DEV_NO_PAGE : FL_DEV_COUNT, b);
     __syncwarp();
     cluster_wait<kCtas>();
     if (b < batch && tell) {
       start[b] = granted ? c : -1;
-      cu[b] = (int)(uint32_t)before;
+      cu[b] = (int)min(row0, (int64_t)INT32_MAX);
     }
     if (granted && tell) x.length[s] = c + n;
     const int count = granted ? need : 0;
@@ -174,7 +185,7 @@ __global__ void __launch_bounds__(kT) extend_kernel(fl_paged_index x, int batch,
       if (count == 1 && (tid >> 5) % kCtas == rank) x.table[(int64_t)s * x.max_pages + block0] = x.free_pages[n_free - 1 - at];
     } else {
       // the granted entries' pages lie one behind the other on the stack, from `base` on
-      const int base = (int)(run >> 32), taken = max(s_taken - base, 0);
+      const int taken = max(s_taken - base, 0);
       jobs.before[tid] = min(at - base, taken);
       jobs.slot[tid] = s;
       jobs.block0[tid] = block0 - (at - base);
@@ -190,11 +201,12 @@ __global__ void __launch_bounds__(kT) extend_kernel(fl_paged_index x, int batch,
       });
       __syncthreads();
     }
-    run += total;
+    rows += (int64_t)(total & kTokens);
+    base += (int)(total >> kPageBit);
   }
   __syncthreads();
   if (tid == 0 && tell) {
-    cu[batch] = (int)(uint32_t)run;
+    cu[batch] = (int)min(rows, (int64_t)INT32_MAX);
     *x.n_free = n_free - s_taken;
   }
 }
