@@ -119,7 +119,8 @@ fl_status fl_paged_slot_map(const fl_paged_index* index, int32_t batch, const in
  * tokens behind them tail rows.  k, v: BF16, row t and head h at k + t token_stride + h
  * head_stride, 128 contiguous channels; strides multiples of 8, pointers 16-byte aligned;
  * k and v share strides.  n_tokens is the rows k and v hold; an entry whose rows pass it is
- * skipped (FL_DEV_COUNT).  A slot may be named once. */
+ * skipped (FL_DEV_COUNT), and so are the first entry with cu[i + 1] < cu[i], told for each such entry, and
+ * all behind it.  A slot may be named once. */
 fl_status fl_paged_append(const fl_paged_index* index, const fl_paged_pool* pool, int32_t batch, const int32_t* slots,
                           const int32_t* start, const int32_t* cu, int32_t n_tokens, const uint16_t* k,
                           const uint16_t* v, int64_t token_stride, int64_t head_stride, void* stream);

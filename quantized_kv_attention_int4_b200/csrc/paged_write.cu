@@ -31,6 +31,7 @@ struct alignas(16) AppendSmem {
   uint32_t sz[kD];                // of each channel: scale and zero, -z, 1 / (15 s)
   float nz[kD], r15[kD];
   int red[kAT / 32];
+  int ascend;  // entries in front of the first whose offsets descend
 };
 
 __device__ __forceinline__ uint32_t bmin2(uint32_t a, uint32_t b) {
@@ -143,14 +144,21 @@ __global__ void __launch_bounds__(kAT, kAppendCtas) append_kernel(PagedAppendArg
   const int heads = a.p.kv_heads;
   const fl_paged_index& x = a.x;
   const bool tell = blockIdx.x == 0;
+  if (tid == 0) sm.ascend = a.batch;
   grid_dep_launch();
+  __syncthreads();
   grid_dep_wait();
   const int copies = (heads + 15) / 16;
-  const int items = paged_scan<kAT>(a.batch, prefix, sm.red, [&](int b) {
+  paged_scan<kAT>(a.batch, prefix, sm.red, [&](int b) {
     const int s = paged_slot(x, a.slots, b, tell);
     const int c = ld(a.start + b), r0 = ld(a.cu + b), r1 = ld(a.cu + b + 1);
+    if (r1 < r0) {
+      atomicMin(&sm.ascend, b);
+      if (tell) paged_error(x, FL_DEV_COUNT, b);
+      return 0;
+    }
     if (s < 0 || c < 0 || r1 == r0) return 0;
-    if (r0 < 0 || r1 < r0 || r1 > a.n_tokens) {
+    if (r0 < 0 || r1 > a.n_tokens) {
       if (tell) paged_error(x, FL_DEV_COUNT, b);
       return 0;
     }
@@ -161,9 +169,12 @@ __global__ void __launch_bounds__(kAT, kAppendCtas) append_kernel(PagedAppendArg
     const int fill = paged_full(c + r1 - r0) - paged_full(c);
     return fill ? 2 * fill * heads : copies;
   });
+  // Offsets that ascend name each row once, so the items of the entries up to there are as few as
+  // the host has checked; behind them sums of 32 bits may have wrapped.
+  const int items = prefix[sm.ascend];
   const int chunk = tid & 15, r0 = tid >> 4;
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int b = paged_find(prefix, a.batch, item), left = item - prefix[b];
+    const int b = paged_find(prefix, sm.ascend, item), left = item - prefix[b];
     const int s = paged_slot(x, a.slots, b, false);
     const int c = ld(a.start + b), row0 = ld(a.cu + b), n = c + ld(a.cu + b + 1) - row0;
     const int full0 = paged_full(c), full1 = paged_full(n);

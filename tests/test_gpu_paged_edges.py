@@ -4,8 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from oracle.paged_oracle import PAGE
-from pagedhelpers import Pair, i32
+from oracle.paged_oracle import D, PAGE
+from pagedhelpers import Pair, bf16, f32, i32
 from quantized_kv_attention_int4_b200 import paged
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +57,46 @@ def test_rows_up_to_the_last_that_offsets_can_name():
         assert pair.c.index.length.tolist() == [0, last if granted else 0, 0]
         assert pair.c.index.n_free.item() == (11 if granted else 12)
         assert pair.c.status()[2] == (1 if granted else 2)
+
+
+# ------------------------------------------------------------------------------- append and read
+def test_append_stops_at_offsets_that_descend():
+    g = gen(2)
+    pair = Pair(5, 4, 20, 2)
+    sl, n = [3, 1, 0, 4, 2], [70, 65, 5, 100, 64]
+    start, cu = pair.c.extend(i32(sl), i32(n))
+    pair.o.extend(sl, n)
+    k, v = bf16(g, 400, 2, D), bf16(g, 400, 2, D)
+    bad = [0, 70, 135, 130, 230, 294]           # the third entry's offsets descend
+    pair.c.append(0, i32(sl), start, i32(bad), k.cuda(), v.cuda())
+    assert pair.c.status() == [paged.FL_DEV_COUNT, 2, 1]
+    pair.o.append(sl[:2], [0, 0], bad[:3], f32(k), f32(v))
+    pool = pair.c.pools[0]
+    for s in (0, 4, 2):
+        assert torch.isnan(pool.tail_k[s]).all() and torch.isnan(pool.tail_v[s]).all()
+    assert not pool.rec[1].any() and not pool.rec[3:].any()     # the first two's blocks are in pages 0 and 2
+    sl[2] = -1                                  # also where the entry is padded
+    pair.c.append(0, i32(sl), start, i32(bad), k.cuda(), v.cuda())
+    assert pair.c.status() == [paged.FL_DEV_COUNT, 2, 1] and torch.isnan(pool.tail_k[4]).all()
+    sl[2] = 0
+    pair.c.append(0, i32(sl), start, cu, k.cuda(), v.cuda())
+    pair.o.append(sl, [0] * 5, np.cumsum([0] + n), f32(k), f32(v))
+    pair.same_bytes()
+    assert pair.c.status()[2] == 0
+
+
+def test_offsets_that_name_the_same_rows_again_and_again():
+    """8192 entries, every other one with all of 2^20 rows of 64 heads: 2^33 items, were they counted."""
+    batch, heads, rows = 8192, 64, 1 << 20
+    x = paged.PagedIndex.empty(1, 16384, 4)
+    pool = paged.PagedPool.empty(x, heads)
+    pool.rec.zero_(), pool.tail_k.zero_(), pool.tail_v.zero_()
+    k = bf16(gen(3), rows // 64, 1, D).cuda().repeat(64, 1, 1).expand(rows, heads, D)
+    cu = torch.zeros(batch + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = rows
+    zeros = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    paged.fl_paged_append(x, pool, zeros, zeros, cu, k, k)
+    # the first entry has its tail; its pages are none (table -1), and every other entry is skipped
+    assert torch.equal(pool.tail_k[0], k[-64:].transpose(0, 1)) and torch.equal(pool.tail_v[0], pool.tail_k[0])
+    assert not pool.rec.any()
+    assert x.status.tolist()[2] == batch // 2 + 16383 * heads
