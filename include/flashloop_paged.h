@@ -100,7 +100,8 @@ fl_status fl_paged_extend(const fl_paged_index* index, int32_t batch, const int3
 
 /* Give every page of each request back (in batch order, block order: the last block's page
  * ends on top of the free stack) and empty the request: length 0, table row's used entries
- * -1.  A slot named twice is released once. */
+ * -1.  A slot named twice is released once.  A used entry that is no page of the pool is told
+ * (FL_DEV_PAGE_RANGE) and given to no one. */
 fl_status fl_paged_release(const fl_paged_index* index, int32_t batch, const int32_t* slots, void* stream);
 
 /* Place and position of tokens start[i] .. start[i] + (cu[i+1] - cu[i]) - 1 of each request,

@@ -8,7 +8,7 @@ import numpy as np
 from . import flashloop_oracle as fo
 
 PAGE, D, REC = 64, 128, 9216
-SLOT_RANGE, SLOT_TWICE, NO_PAGE, TOO_LONG, COUNT = 16, 17, 18, 19, 20
+SLOT_RANGE, SLOT_TWICE, NO_PAGE, TOO_LONG, COUNT, PAGE_RANGE = 16, 17, 18, 19, 20, 21
 
 
 def full(n: int) -> int:
@@ -107,7 +107,11 @@ class PagedOracle:
             if s < 0:
                 continue
             for j in range(blocks(int(self.length[s]))):
-                self.free.append(int(self.table[s, j]))
+                p = int(self.table[s, j])
+                if 0 <= p < self.pages:
+                    self.free.append(p)
+                else:
+                    self.errors.append((PAGE_RANGE, b))
                 self.table[s, j] = -1
             self.length[s] = 0
 

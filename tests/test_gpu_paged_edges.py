@@ -59,6 +59,44 @@ def test_rows_up_to_the_last_that_offsets_can_name():
         assert pair.c.status()[2] == (1 if granted else 2)
 
 
+@pytest.mark.parametrize("slots,max_pages", [(20, 10), (120, 30), (1100, 6)])
+def test_damaged_table_entries_are_given_to_no_one(slots, max_pages):
+    """Release of tables with entries that are no pages: the others come back in order, the next
+    requests get pages only.  In one block, in a cluster, and over several chunks."""
+    r = np.random.default_rng(slots)
+    pages = slots * max_pages // 2
+    pair = Pair(slots, max_pages, pages, 1)
+    x, o = pair.c.index, pair.o
+    n = r.integers(0, 64 * max_pages // 2, slots)
+    n[0], n[1] = 64 * max_pages // 2, 65
+    pair.c.extend(None, i32(n))
+    o.extend(None, n)
+    hit = [s for s in range(slots) if s < 2 or r.random() < 0.1 and n[s] > 0]
+    for i, s in enumerate(hit):
+        j = int(r.integers(0, -(-n[s] // PAGE)))
+        o.table[s, j] = x.table[s, j] = (-1, pages, -5, M)[i % 4]
+    order = r.permutation(slots)
+    order[3] = -1
+    order[[5, 6]] = 0, 1                        # damaged rows among them, whatever the order
+    for part in (order[: slots // 2], order[slots // 2:]):
+        pair.c.release(i32(part))
+        o.release(part, len(part))
+        pair.same_index()
+    n_free = int(x.n_free.item())
+    assert n_free < pages
+    code, detail, count = pair.c.status()
+    assert count == len(o.errors) and (code, detail) in o.errors and paged.FL_DEV_PAGE_RANGE in {c for c, _ in o.errors}
+    o.errors.clear()
+    sl = [s for s in range(slots) if o.length[s] == 0]
+    n = np.full(len(sl), 64)
+    start, cu = pair.c.extend(i32(sl), i32(n))
+    ostart, _ = o.extend(sl, n)
+    assert start.tolist() == ostart.tolist()
+    pair.same_index()
+    got = [int(x.table[s, 0]) for s, b in zip(sl, ostart) if b >= 0]
+    assert len(set(got)) == len(got) and min(got) >= 0 and max(got) < pages
+
+
 # ------------------------------------------------------------------------------- append and read
 def test_append_stops_at_offsets_that_descend():
     g = gen(2)
