@@ -351,6 +351,9 @@ __global__ void __launch_bounds__(kTT) topk_kernel(PagedAttnArgs a) {
   }
 }
 
+std::atomic<bool> g_attr_done[kMaxDevices];
+std::mutex g_attr_mu;
+
 }  // namespace
 
 uint64_t paged_select_bytes(const fl_paged_index& x, const fl_paged_pool& p, int batch) {
@@ -363,6 +366,11 @@ cudaError_t launch_paged_select(const PagedAttnArgs& a, cudaStream_t s) {
   if (sms <= 0) return cudaErrorInvalidDevice;
   const bool scored = a.keep < a.x.max_pages;  // otherwise every request keeps all it has
   if (scored) {
+    // the queries and the offsets of the largest batches together pass what a launch has unasked
+    const cudaError_t r = once_per_device(g_attr_done, g_attr_mu, [](int) {
+      return cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (FL_PAGED_MAX_BATCH + 1) * 4);
+    });
+    if (r != cudaSuccess) return r;
     const int64_t items = (int64_t)a.batch * ((a.x.max_pages + kChunk - 1) / kChunk) * a.p.kv_heads;
     const int grid = (int)(items < 2 * sms ? items : 2 * sms);
     const cudaError_t e = launch_pdl(score_kernel, dim3(grid), dim3(kST), (size_t)(a.batch + 1) * 4, s, a);

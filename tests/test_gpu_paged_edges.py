@@ -138,3 +138,47 @@ def test_offsets_that_name_the_same_rows_again_and_again():
     assert torch.equal(pool.tail_k[0], k[-64:].transpose(0, 1)) and torch.equal(pool.tail_v[0], pool.tail_k[0])
     assert not pool.rec.any()
     assert x.status.tolist()[2] == batch // 2 + 16383 * heads
+
+
+# ------------------------------------------------------------------------------- the largest batches
+@pytest.mark.parametrize("batch", [8183, 8184, paged.MAX_BATCH])
+def test_the_largest_batches_do_what_their_parts_do(batch):
+    """Every call on a whole batch of up to 8192 entries against the same calls on 128 entries at a time."""
+    r = np.random.default_rng(batch)
+    g = gen(4, batch)
+    kv, heads = 2, 6
+    n = r.integers(0, 260, batch)
+    x = paged.PagedIndex.empty(batch, 5, int(sum(-(-n // PAGE))))
+    sl = i32(r.permutation(batch))
+    start, cu = (torch.empty(batch + e, dtype=torch.int32, device="cuda") for e in (0, 1))
+    paged.fl_paged_extend(x, sl, i32(n), start, cu)
+    assert not start.any() and cu.tolist() == np.cumsum([0, *n]).tolist() and x.n_free.item() == 0
+    t = int(n.sum())
+    k, v = (bf16(g, 4096, kv, D).cuda().repeat(-(-t // 4096), 1, 1)[:t] for _ in range(2))
+    q = bf16(g, batch, heads, D, scale=1.5).cuda()
+    pools = [paged.PagedPool.empty(x, kv) for _ in range(2)]
+    for p in pools:
+        p.rec.zero_(), p.tail_k.zero_(), p.tail_v.zero_()
+    place, pos = (torch.full((2, t), -7, dtype=torch.int32, device="cuda") for _ in range(2))
+    sel = torch.full((2, batch, kv, 2), -7, dtype=torch.int32, device="cuda")
+    o = torch.full((4, batch, heads, D), 7.0, device="cuda")
+    ws = [paged.workspace(x, pools[0], b, heads) for b in (batch, 128)]
+    for i, step in enumerate((batch, 128)):
+        for b in range(0, batch, step):
+            e = slice(b, min(b + step, batch))
+            at = cu[e.start: e.stop + 1].contiguous()
+            paged.fl_paged_append(x, pools[i], sl[e], start[e], at, k, v)
+            paged.fl_paged_slot_map(x, sl[e], start[e], at, place[i], pos[i])
+            paged.fl_paged_select(x, pools[i], sl[e], q[e], sel[i, e], ws[i])
+            paged.fl_paged_attn_decode(x, pools[i], sl[e], q[e], o[i, e], ws[i])
+            paged.fl_paged_attn_decode(x, pools[i], sl[e], q[e], o[2 + i, e], ws[i], sel=sel[i, e])
+    for name in ("rec", "tail_k", "tail_v"):
+        assert torch.equal(getattr(pools[0], name), getattr(pools[1], name)), name
+    assert torch.equal(place[0], place[1]) and torch.equal(pos[0], pos[1]) and not (place == -7).any()
+    assert torch.equal(sel[0], sel[1]) and (sel >= -1).all()
+    for i in (0, 2):
+        # each side within check_attention's 4e-6 of the exact output, whatever the cuts between warps
+        assert ((o[i] - o[i + 1]).norm(dim=-1) <= 8e-6 * o[i].norm(dim=-1)).all()
+    assert x.status.tolist()[2] == 0
+    paged.fl_paged_release(x, sl)
+    assert not x.length.any() and sorted(x.free_pages.tolist()) == list(range(x.pages))
