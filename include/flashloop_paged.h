@@ -159,8 +159,9 @@ fl_status fl_paged_select(const fl_paged_index* index, const fl_paged_pool* pool
  * aligned, strides multiples of 8); query heads g kv .. of a group share key-value head
  * h = head / (q_heads / kv_heads), q_heads a multiple of kv_heads.  o: fp32, strides
  * multiples of 4, 16-byte aligned, rows that do not overlap.  lse: NULL or fp32 [batch][q_heads], the base-2 logarithm
- * of the sum of 2^score with scores in base 2 (q.k log2(e) / sqrt(128)).  A request of no
- * tokens gives o = 0 and lse = -inf; rows of padded entries are left as they were.  Sums in
+ * of the sum of 2^score with scores in base 2 (q.k log2(e) / sqrt(128)).  A token whose score is
+ * -inf has no weight; a request of no tokens, or of such tokens alone, gives o = 0 and
+ * lse = -inf; rows of padded entries are left as they were.  Sums in
  * fp32; results do not depend on what else is in the batch beyond fp32 rounding, and are the
  * same for the same call. */
 fl_status fl_paged_attn_decode(const fl_paged_index* index, const fl_paged_pool* pool, int32_t batch,

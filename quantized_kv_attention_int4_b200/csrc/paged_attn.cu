@@ -225,6 +225,8 @@ struct State {
   // weights are p = 2^(score - m), m one number for all lanes of a head; this lane's sums
   float m[kTiles], l[kTiles], z0[kTiles], z1[kTiles];
 
+  // m, or 0 before the first score above -inf: those of -inf then weigh 0, not NaN
+  __device__ __forceinline__ float base(int t) const { return m[t] == -INFINITY ? 0.f : m[t]; }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
@@ -435,7 +437,7 @@ __device__ __forceinline__ void block_unit(unsigned st, Query<kTiles>& qr, State
   // values' scales are below 2^(ev - 14): p s < 2^15
   s.raise(top, 29.f - (float)max((int)(vtop >> 26) & 31, 1));
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) off[t] -= s.m[t];
+  for (int t = 0; t < kTiles; ++t) off[t] -= s.base(t);
   uint32_t bv[kTiles][2][8];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
@@ -538,7 +540,7 @@ __device__ __forceinline__ void tail_unit(unsigned st, int live, const Query<kTi
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       // rows behind the last: exactly 0, whatever their scores
-      const float p = i + 8 * k < live ? ex2(c[t][k] - s.m[t]) : 0.f;
+      const float p = i + 8 * k < live ? ex2(c[t][k] - s.base(t)) : 0.f;
       s.l[t] += p;
       const float hi = __bfloat162float(__float2bfloat16_rn(p)), r1 = p - hi;  // parts of 8 bits
       const float mid = __bfloat162float(__float2bfloat16_rn(r1));

@@ -4,8 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from oracle.paged_oracle import D, PAGE
-from pagedhelpers import Pair, bf16, f32, i32
+from oracle.paged_oracle import D, PAGE, full
+from pagedhelpers import Pair, bf16, check_attention, f32, i32
 from quantized_kv_attention_int4_b200 import paged
 
 pytestmark = pytest.mark.gpu
@@ -138,6 +138,46 @@ def test_offsets_that_name_the_same_rows_again_and_again():
     assert torch.equal(pool.tail_k[0], k[-64:].transpose(0, 1)) and torch.equal(pool.tail_v[0], pool.tail_k[0])
     assert not pool.rec.any()
     assert x.status.tolist()[2] == batch // 2 + 16383 * heads
+
+
+# ------------------------------------------------------------------------------- attention
+@pytest.mark.parametrize("kv,group", [(1, 1), (2, 4), (1, 7)])
+def test_tokens_of_infinitely_low_scores_have_no_weight(kv, group):
+    """Blocks whose zero is -inf (keys below the 16-bit numbers) and tail rows of -inf: wherever
+    they stand, first in a request or in a warp's part, the others' softmax is as without them."""
+    g = gen(5, kv, group)
+    lengths = [64 * 30 + 5, 65, 130, 84, 64 * 4 + 17, 1, 64 * 3 + 2, 33]
+    pair = Pair(len(lengths), 32, 60, kv, kv * group)
+    cu = np.concatenate([[0], np.cumsum(lengths)])
+    k, v = bf16(g, int(cu[-1]), kv, D), bf16(g, int(cu[-1]), kv, D)
+    low = -66048.0 - 512.0 * (torch.arange(64) % 8)
+    for b, n in enumerate(lengths):
+        for j in range(full(n)):
+            if b in (1, 6) or j % 2 == 0:
+                k[cu[b] + 64 * j: cu[b] + 64 * j + 64, :, 0] = low[:, None].bfloat16()
+    for b, rows in ((3, range(64, 80)), (4, range(256, 272)), (5, [0]), (6, [192, 193]), (7, range(0, 32))):
+        k[[int(cu[b]) + t for t in rows], :, 0] = float("-inf")
+    start, c = pair.c.extend(None, i32(lengths))
+    pair.c.append(0, None, start, c, k.cuda(), v.cuda())
+    s, oc = pair.o.extend(None, lengths)
+    with np.errstate(over="ignore"):
+        pair.o.append(None, s, oc, f32(k), f32(v))
+    pair.same_bytes()
+    q = bf16(g, len(lengths), kv * group, D, scale=1.5)
+    q[..., 0] = q[..., 0].abs() + 0.125
+    o = torch.full(q.shape, float("nan"), device="cuda")
+    lse = torch.full(q.shape[:2], float("nan"), device="cuda")
+    pair.c.attend(0, None, q.cuda(), o, lse)
+    for b in (5, 6):
+        assert not o[b].any() and torch.isneginf(lse[b]).all()
+    live = [b for b in range(len(lengths)) if b not in (5, 6)]
+    check_attention(pair, live, q[live], o[live], lse[live])
+    for b in live:
+        for h in range(kv):
+            _, want = pair.o.attend(b, h, q[b, h * group: (h + 1) * group].double().numpy())
+            # scores of up to 2^6 in base 2, each a sum of 128 products: 132 half steps at most
+            assert np.abs(lse[b, h * group: (h + 1) * group].cpu().numpy() - want).max() <= 132 * 2.0 ** -24 * 64
+    assert pair.c.status()[2] == 0
 
 
 # ------------------------------------------------------------------------------- the largest batches
