@@ -328,7 +328,8 @@ __global__ void __launch_bounds__(kMapT) slot_map_kernel(fl_paged_index x, int b
   const int32_t* off = held ? s_cu : cu;
   const int t0 = (blockIdx.x * kMapT + threadIdx.x) * kMapRows;
   const int begin = off[0], end = min(off[batch], n_tokens);
-  if (t0 + kMapRows <= begin || t0 >= end) return;
+  // (the last rows of 2^31 - 1: the thread's end is no number of 32 bits)
+  if ((int64_t)t0 + kMapRows <= begin || t0 >= end) return;
   int at[kMapRows], where[kMapRows];
   int b = -1, first = 0, last = -1;  // rows [first, last) are entry b's
   int s = -1, from = -1, n = 0, full = 0;
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(kMapT) slot_map_kernel(fl_paged_index x, int b
     }
     where[y] = page * FL_PAGE + (at[y] & 63);
   }
-  if (vec && t0 >= begin && t0 + kMapRows <= end) {
+  if (vec && t0 >= begin && (int64_t)t0 + kMapRows <= end) {
     if (place) *reinterpret_cast<int4*>(place + t0) = make_int4(where[0], where[1], where[2], where[3]);
     if (pos) *reinterpret_cast<int4*>(pos + t0) = make_int4(at[0], at[1], at[2], at[3]);
     return;

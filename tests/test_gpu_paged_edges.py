@@ -97,6 +97,14 @@ def test_damaged_table_entries_are_given_to_no_one(slots, max_pages):
     assert len(set(got)) == len(got) and min(got) >= 0 and max(got) < pages
 
 
+def test_slot_map_of_the_last_rows_that_offsets_can_name():
+    x = paged.PagedIndex.empty(2, 4, 8)
+    paged.fl_paged_extend(x, None, i32([90, 100]), i32([0, 0]), i32([0, 0, 0]))
+    pos = torch.full((M,), -7, dtype=torch.int32, device="cuda")
+    paged.fl_paged_slot_map(x, None, i32([3, 40]), i32([M - 11, M - 9, M]), None, pos)
+    assert pos[M - 14:].tolist() == [-7] * 3 + [3, 4] + list(range(40, 49))
+
+
 # ------------------------------------------------------------------------------- append and read
 def test_append_stops_at_offsets_that_descend():
     g = gen(2)
