@@ -4,9 +4,10 @@ import numpy as np
 import pytest
 import torch
 
-from oracle.paged_oracle import D, PAGE, full
+from oracle import flashloop_oracle as fo
+from oracle.paged_oracle import D, PAGE, REC, full
 from pagedhelpers import Pair, bf16, check_attention, f32, i32
-from quantized_kv_attention_int4_b200 import paged
+from quantized_kv_attention_int4_b200 import abi, paged
 
 pytestmark = pytest.mark.gpu
 
@@ -15,6 +16,54 @@ M = 2 ** 31 - 1
 
 def gen(*key):
     return torch.Generator().manual_seed(sum((i + 1) * 104729 * int(k) for i, k in enumerate(key)) + 71)
+
+
+def random_cache(lengths, max_pages, kv, group, seed, kinds=None):
+    """A pair whose requests hold random records and tails (of `kinds` different key scales and
+    zeros, if given): (pair, slots)."""
+    r = np.random.default_rng(seed)
+    pages = sum(-(-n // PAGE) for n in lengths) + 3
+    pair = Pair(len(lengths) + 1, max_pages, pages, kv, kv * group, max_batch=len(lengths))
+    slots = r.permutation(len(lengths) + 1)[: len(lengths)].tolist()
+    start, _ = pair.c.extend(i32(slots), i32(lengths))
+    ostart, _ = pair.o.extend(slots, lengths)
+    assert start.tolist() == ostart.tolist() == [0] * len(lengths)
+    rec = r.integers(0, 256, (pages, kv, REC), dtype=np.uint8)
+    words = rec[..., 8192:].view(np.float16).reshape(pages, kv, 256, 2)     # 128 of values, 128 of channels
+    words[..., 0] = 0.2 * np.exp(0.3 * r.standard_normal(words.shape[:3]))
+    words[..., 1] = -7.5 * words[..., 0] + 0.3 * r.standard_normal(words.shape[:3])
+    if kinds:
+        words[:, :, 128:] = words[r.integers(0, kinds, pages), :, 128:]
+    pair.o.rec[:] = rec
+    tail = torch.from_numpy(r.standard_normal(pair.o.tail.shape).astype(np.float32)).bfloat16()
+    pair.o.tail[:] = tail.float().numpy()
+    pool = pair.c.pools[0]
+    pool.rec.copy_(torch.from_numpy(rec))
+    pool.tail_k.copy_(tail[0]), pool.tail_v.copy_(tail[1])
+    return pair, slots
+
+
+def best_blocks(pair, s, h, q, keep):
+    """The selection by its definition in fp64, blocks that are not finite behind all others."""
+    f = full(int(pair.o.length[s]))
+    if f <= keep:
+        return list(range(f))
+    sz = pair.o.rec[pair.o.table[s, :f], h, 8704:].copy().view(np.float16).astype(np.float64).reshape(f, D, 2)
+    lo, hi = sz[..., 1], sz[..., 1] + 15 * sz[..., 0]
+    score = np.maximum(q[:, None] * lo, q[:, None] * hi).sum(-1).max(0)
+    bad = ~np.isfinite(sz).all((1, 2))
+    return sorted(sorted(range(f), key=lambda j: (bad[j], 0.0 if bad[j] else -score[j], j))[:keep])
+
+
+def check_selection(pair, slots, q, sel, keep):
+    """sel int32 [batch][kv][keep] of the GPU; returns the chosen blocks."""
+    qn, got, chosen = q.double().numpy(), sel.cpu().numpy(), []
+    group = q.shape[1] // pair.kv
+    for b, s in enumerate(slots):
+        chosen.append([best_blocks(pair, s, h, qn[b, h * group: (h + 1) * group], keep) for h in range(pair.kv)])
+        for h, want in enumerate(chosen[-1]):
+            assert got[b, h].tolist() == want + [-1] * (keep - len(want)), (b, h)
+    return chosen
 
 
 # ------------------------------------------------------------------------------- tables
@@ -148,7 +197,87 @@ def test_offsets_that_name_the_same_rows_again_and_again():
     assert x.status.tolist()[2] == batch // 2 + 16383 * heads
 
 
+@pytest.mark.parametrize("kv", [17, 33])
+def test_append_of_more_than_16_heads(kv):
+    """Requests that fill no block are one item per 16 heads: the last item has fewer."""
+    g = gen(6, kv)
+    pair = Pair(3, 3, 8, kv)
+    for slots, n in (([0, 2, 1], [1, 64, 30]), ([2, 1], [1, 3]), ([0, 1], [63, 31]), (None, [1, 2, 3])):
+        pair.step(slots, n, g)
+        pair.same_bytes()
+    assert pair.c.status()[2] == 0
+
+
+@pytest.mark.parametrize("kv,n,active", [(1, 77, 1), (3, 700, 130), (2, 64 * 9, 300)])
+def test_rows_read_back_feed_the_prefill_attention(kv, n, active):
+    """A cached prefix read into [head][token] rows, and the attention of its last tokens over them."""
+    g = gen(7, kv, n)
+    pair = Pair(2, 16, 16, kv)
+    pair.step([1], [n], g)
+    k, v = torch.full((2, kv, n, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    place, pos = pair.c.places(i32([1]), i32([0]), i32([0, n]), n)
+    paged.fl_paged_read(pair.c.index, pair.c.pools[0], place, k.transpose(0, 1), v.transpose(0, 1))
+    for h in range(kv):
+        for got, ref in zip((k, v), pair.o.keys_values(1, h)):
+            assert torch.equal(got[h].cpu(), torch.from_numpy(ref.astype(np.float32)).bfloat16())
+    q = bf16(g, kv, active, D)
+    o = torch.full((kv, active, D), float("nan"), device="cuda")
+    abi.fl_prefill_attn_sparse(q.cuda(), pos[n - active:].contiguous(), k, v, o)
+    ref = fo.prefill_attention(f32(q), np.arange(n - active, n), f32(k), f32(v))
+    # the prefill attention's own tolerance, per row (test_gpu_prefill.py)
+    assert (np.abs(o.cpu().numpy() - ref).max(-1) <= 2e-3 * np.abs(ref).max(-1)).all()
+
+
 # ------------------------------------------------------------------------------- attention
+MIXED = [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 300, 1000, 1345, 20000, 9000, 3000]
+
+
+@pytest.mark.parametrize("kv,group,max_pages,keep", [(2, 5, 460, 420), (1, 6, 900, 840), (4, 8, 320, 210), (2, 9, 460, 420),
+                                                     (1, 12, 900, 840), (1, 17, 900, 840)])
+def test_large_calls_of_many_heads_a_group(kv, group, max_pages, keep):
+    """Groups above 4 where the call can hold more than 8 units a warp: eight heads a segment, in one
+    segment and in several, every length, pieces cut between warps and between CTAs; the whole
+    cache, the best blocks, and any blocks."""
+    few = 8 * 12 * torch.cuda.get_device_properties(0).multi_processor_count
+    assert len(MIXED) * kv * (keep + 4) > few and keep < max_pages
+    g = gen(8, kv, group)
+    pair, slots = random_cache(MIXED, max_pages, kv, group, 8 * kv + group)
+    q = bf16(g, len(slots), kv * group, D, scale=1.5)
+    o, lse = torch.full(q.shape, float("nan"), device="cuda"), torch.full(q.shape[:2], float("nan"), device="cuda")
+    pair.c.attend(0, i32(slots), q.cuda(), o, lse)
+    check_attention(pair, slots, q, o, lse)
+    again = torch.empty_like(o)
+    pair.c.attend(0, i32(slots), q.cuda(), again)
+    assert torch.equal(again, o)
+    sel = pair.c.select(0, i32(slots), q.cuda(), keep)
+    best = check_selection(pair, slots, q, sel, keep)
+    r = np.random.default_rng(group)
+    some = [[sorted(r.permutation(full(n))[: full(n) * 2 // 3].tolist()) for _ in range(kv)] for n in MIXED]
+    rows = torch.tensor([[c + [-1] * (keep - len(c)) for c in head] for head in some], dtype=torch.int32, device="cuda")
+    for chosen, picked in ((best, sel), (some, rows)):
+        o.fill_(float("nan")), lse.fill_(float("nan"))
+        paged.fl_paged_attn_decode(pair.c.index, pair.c.pools[0], i32(slots), q.cuda(), o, pair.c.ws, lse=lse, sel=picked)
+        check_attention(pair, slots, q, o, lse, chosen)
+    assert pair.c.status()[2] == 0
+
+
+@pytest.mark.parametrize("group", [7, 11])
+def test_large_calls_of_many_entries_and_heads(group):
+    """The same kernels behind the block-wide scan of more than 128 entries, padded ones among them."""
+    r = np.random.default_rng(group)
+    lengths = r.integers(0, 400, 300).tolist()
+    assert 300 * (46 + 4) > 8 * 12 * torch.cuda.get_device_properties(0).multi_processor_count
+    pair, slots = random_cache(lengths, 46, 1, group, group)
+    named = np.array(slots)
+    named[r.random(300) < 0.1] = -1
+    q = bf16(gen(9, group), 300, group, D, scale=1.5)
+    o, lse = torch.full(q.shape, 7.0, device="cuda"), torch.full(q.shape[:2], 7.0, device="cuda")
+    pair.c.attend(0, i32(named), q.cuda(), o, lse)
+    live = np.flatnonzero(named >= 0)
+    check_attention(pair, named[live], q[live], o[live], lse[live])
+    assert (o[named < 0] == 7).all() and (lse[named < 0] == 7).all()
+
+
 @pytest.mark.parametrize("kv,group", [(1, 1), (2, 4), (1, 7)])
 def test_tokens_of_infinitely_low_scores_have_no_weight(kv, group):
     """Blocks whose zero is -inf (keys below the 16-bit numbers) and tail rows of -inf: wherever
@@ -186,6 +315,65 @@ def test_tokens_of_infinitely_low_scores_have_no_weight(kv, group):
             # scores of up to 2^6 in base 2, each a sum of 128 products: 132 half steps at most
             assert np.abs(lse[b, h * group: (h + 1) * group].cpu().numpy() - want).max() <= 132 * 2.0 ** -24 * 64
     assert pair.c.status()[2] == 0
+
+
+# ------------------------------------------------------------------------------- selection
+LONG = [64 * 515 + 9, 64 * 300, 64 * 257 + 64, 64 * 256 + 1, 64 * 130 + 5, 64 * 65 + 2, 64 * 64 + 2, 64 * 9, 70, 64, 0]
+
+
+@pytest.mark.parametrize("max_pages", [257, 258, 520])
+@pytest.mark.parametrize("kv,group,keep", [(1, 1, 1), (2, 4, 52), (1, 11, 64), (1, 2, 255), (3, 1, 256)])
+def test_selection_of_long_requests(max_pages, kv, group, keep):
+    """Requests of up to 515 blocks and short ones beside them, in tables on both sides of the
+    width that decides how blocks are ordered, several chunks of 64 blocks a head."""
+    lengths = [min(n, 64 * max_pages) for n in LONG]
+    pair, slots = random_cache(lengths, max_pages, kv, group, max_pages + keep)
+    q = bf16(gen(10, kv, group, keep), len(slots), kv * group, D, scale=1.5)
+    check_selection(pair, slots, q, pair.c.select(0, i32(slots), q.cuda(), keep), keep)
+    assert pair.c.status()[2] == 0
+
+
+@pytest.mark.parametrize("max_pages,blocks", [(260, 64), (260, 258), (520, 257), (520, 515), (4100, 4001)])
+@pytest.mark.parametrize("kinds", [1, 2, 7])
+def test_equal_scores_over_many_blocks_go_to_the_lower_ones(max_pages, blocks, kinds):
+    """Few different scores, ties across warps, chunks and passes: all equal, and a handful of values;
+    from one block kept to all but one."""
+    n = 64 * blocks + 3
+    pair, slots = random_cache([n, n // 2, n], max_pages, 1, 2, blocks + kinds, kinds)
+    q = bf16(gen(11, blocks, kinds), 3, 2, D)
+    for keep in sorted({1, 5, 31, 64, blocks // 2, min(256, blocks - 1), blocks - 1}):
+        check_selection(pair, slots, q, pair.c.select(0, i32(slots), q.cuda(), keep), keep)
+    q[:] = 0                                    # every score is 0
+    check_selection(pair, slots, q, pair.c.select(0, i32(slots), q.cuda(), 40), 40)
+
+
+@pytest.mark.parametrize("max_pages", [250, 400])
+def test_blocks_that_are_not_finite_are_the_last_taken(max_pages):
+    pair, slots = random_cache([64 * 240 + 1, 64 * 100], max_pages, 2, 3, max_pages)
+    r = np.random.default_rng(max_pages)
+    ksz = pair.o.rec[..., 8704:].view(np.float16)
+    for bad in (np.inf, -np.inf, np.nan):
+        pages = r.permutation(len(ksz))[:60]
+        ksz[pages, r.integers(0, 2, 60), r.integers(0, 256, 60)] = bad
+    pair.c.pools[0].rec.copy_(torch.from_numpy(pair.o.rec))
+    q = bf16(gen(12, max_pages), 2, 6, D)
+    for keep in (3, 60, 230, 239):              # the last ones have to take some of them
+        check_selection(pair, slots, q, pair.c.select(0, i32(slots), q.cuda(), keep), keep)
+
+
+def test_selection_of_forty_requests():
+    r = np.random.default_rng(40)
+    lengths = r.integers(0, 64 * 90, 40).tolist()
+    for max_pages in (95, 300):
+        pair, slots = random_cache(lengths, max_pages, 2, 4, max_pages)
+        named = np.array(slots)
+        named[[4, 17, 39]] = -1
+        q = bf16(gen(13), 40, 8, D, scale=1.5)
+        sel = torch.full((40, 2, 12), -9, dtype=torch.int32, device="cuda")
+        paged.fl_paged_select(pair.c.index, pair.c.pools[0], i32(named), q.cuda(), sel, pair.c.ws)
+        live = np.flatnonzero(named >= 0)
+        check_selection(pair, named[live], q[live], sel[torch.from_numpy(live).cuda()], 12)
+        assert (sel[[4, 17, 39]] == -9).all()
 
 
 # ------------------------------------------------------------------------------- the largest batches
