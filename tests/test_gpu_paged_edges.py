@@ -8,6 +8,7 @@ from oracle import flashloop_oracle as fo
 from oracle.paged_oracle import D, PAGE, REC, full
 from pagedhelpers import Pair, bf16, check_attention, f32, i32
 from quantized_kv_attention_int4_b200 import abi, paged
+from quantized_kv_attention_int4_b200.cache import FlashLoopCache
 
 pytestmark = pytest.mark.gpu
 
@@ -206,6 +207,32 @@ def test_append_of_more_than_16_heads(kv):
         pair.step(slots, n, g)
         pair.same_bytes()
     assert pair.c.status()[2] == 0
+
+
+def test_records_are_the_single_sequence_encoders_whatever_the_values():
+    """NaN, infinities, numbers beyond and below the 16-bit ones and zeros of both signs, alone and
+    mixed in a group: the same bytes as fl_encode_base (whose quantiser the header names)."""
+    r = np.random.default_rng(17)
+    heads, n = 2, 64 * 40
+    odd = np.array([np.nan, np.inf, -np.inf, 7e4, -7e4, 3e38, -3e38, 1e-40, -1e-40, 0.0, -0.0, 65504.0, 65520.0, -65535.0])
+    kv = []
+    for _ in range(2):
+        x = r.standard_normal((heads, n, D)) * np.exp2(r.integers(-20, 16, (heads, n // 64, D)).repeat(64, 1))
+        x = np.where(r.random(x.shape) < r.choice([0.0, 0.01, 0.3], (heads, n // 64, D)).repeat(64, 1), r.choice(odd, x.shape), x)
+        x[0, :64, :14] = odd                    # whole groups of one value
+        kv.append(torch.from_numpy(x).bfloat16().cuda())
+    k, v = kv
+    cache = FlashLoopCache(1, heads, 2, n)
+    abi.fl_encode_base(cache.dims, cache.buf, 0, 0, k, v)
+    want = cache.raw("brec", 0)[: heads * n // 64 * REC].view(heads, n // 64, REC)
+    pair = Pair(1, n // 64 + 1, n // 64 + 1, heads)
+    rows = lambda t: torch.cat([t, t[:, :1]], 1).transpose(0, 1)  # noqa: E731
+    start, cu = pair.c.extend(i32([0]), i32([n + 1]))
+    pair.c.append(0, i32([0]), start, cu, rows(k), rows(v))
+    got = pair.c.pools[0].rec[pair.c.index.table[0, : n // 64].long()].transpose(0, 1)
+    for t in range(heads):
+        for j in range(n // 64):
+            assert torch.equal(got[t, j], want[t, j]), (t, j)
 
 
 @pytest.mark.parametrize("kv,n,active", [(1, 77, 1), (3, 700, 130), (2, 64 * 9, 300)])
