@@ -147,7 +147,8 @@ fl_status fl_paged_workspace_init(void* ws, size_t ws_bytes, void* stream);
  * With lo_c = z_c and hi_c = z_c + 15 s_c from the record's key groups
  *     score(block) = max over the group's queries q of sum_c max(q_c lo_c, q_c hi_c),
  * the largest score any key of the block could have; summed in fp64, ties to the lower
- * block; blocks whose scales or zeros are not finite, or whose score is NaN, come last.  q as in fl_paged_attn_decode. */
+ * block; blocks whose scales or zeros are not finite, or whose score is NaN, come last (an
+ * infinite q makes it so wherever a channel's bounds differ in sign).  q as in fl_paged_attn_decode. */
 fl_status fl_paged_select(const fl_paged_index* index, const fl_paged_pool* pool, int32_t batch, const int32_t* slots,
                           int32_t q_heads, const uint16_t* q, int64_t q_batch_stride, int64_t q_head_stride,
                           int32_t keep, int32_t* sel, void* ws, size_t ws_bytes, void* stream);
@@ -163,7 +164,9 @@ fl_status fl_paged_select(const fl_paged_index* index, const fl_paged_pool* pool
  * -inf has no weight; a request of no tokens, or of such tokens alone, gives o = 0 and
  * lse = -inf; rows of padded entries are left as they were.  Sums in
  * fp32; results do not depend on what else is in the batch beyond fp32 rounding, and are the
- * same for the same call. */
+ * same for the same call.  A head's q is held as binary16 numbers of one common power of two
+ * (exactly, within 2^-16 of its largest channel): a channel below that is rounded, which shows
+ * where its keys are 2^10 times the other channels' or more. */
 fl_status fl_paged_attn_decode(const fl_paged_index* index, const fl_paged_pool* pool, int32_t batch,
                                const int32_t* slots, int32_t q_heads, const uint16_t* q, int64_t q_batch_stride,
                                int64_t q_head_stride, const int32_t* sel, int32_t keep, float* o,

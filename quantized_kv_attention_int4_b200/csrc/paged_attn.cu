@@ -35,10 +35,11 @@
 //   Tail rows are BF16: q.k exactly so, p in three BF16 parts (2^-24).
 //
 // Measured (device time; floor at the card's measured 6.56 TB/s): 16 requests of 32768, 8 x 4
-// heads 130 us (607 MB, 4.7 TB/s; floor 93), 64 of up to 8191, 16 heads 42 us (137 MB; 21), one of
-// 256 7.7 us.  Long calls are bound by instructions: 1,300 a block and warp, 78 % of the issue
-// slots while the stream lasts (copies alone: 109 us); short ones by the trips to memory that
-// wait for one another, lengths, table, record, join.
+// heads 131 us (607 MB, 4.6 TB/s; floor 93), 64 of up to 8191, 16 heads 42.6 us (137 MB; 21), one of
+// 256 7.7 us.  Without the blocks' arithmetic, all else as it is, the first two take 100 and 39 us:
+// the long call is bound by its instructions (1,240 a block and warp, 59 % of the issue slots over
+// a launch), the mixed one by its copies and, as short ones are, by the trips to memory that wait for
+// one another, lengths, table, record, join.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -334,7 +335,9 @@ struct Query {
   }
   // Fit the shift to a record whose largest scale has exponent field ek (below 2^(ek - 14)):
   // products q s stay below 2^15, and where they can above 2^3, far from binary16's last bit
-  // 2^-24.  Rarely changes: records' scales are much alike.
+  // 2^-24.  Rarely changes: records' scales are much alike.  Channels are held to 2^-25 of this
+  // common range, so what is far below the head's largest is worth less: at 2^-17 of it against keys
+  // 2^11 times the other channels' outputs are off by 1.2e-6, at 2^-20 and 2^14 by 1.2e-4.
   __device__ __forceinline__ void fit(int ek) {
     if (shift + ek <= 28 && (shift + ek >= 18 || shift == 14)) return;
     const int by = min(14, 25 - ek) - shift, a = by / 2, b = by - a;

@@ -8,10 +8,11 @@
 // simply loses its top P and every entry's place on it is P_i - need_i.  The work is a scan over
 // at most 8192 entries and 8 bytes per page, and its time is the launch and four dependent trips
 // to memory.  Up to 128 entries of not too many pages one block of 128 threads does it (whose
-// barriers cost half of 1024 threads': 64 decode steps with their slot map 5.7 us on the device),
-// else a cluster of eight blocks that share the moving of the pages out (512 requests of up to
-// 8192 tokens leave and as many come, with their slot map: 14.4 us in blocks of 512 threads, 16.4
-// of 1024, 19.4 of 256; one block of 1024 threads 25.4).  The kernels here start while their
+// barriers cost half of 1024 threads': 64 decode steps with their slot map 5.7 us on the device in
+// a table of 256 columns, 6.7 by the cluster in one of 8192), else a cluster of eight blocks that share
+// the moving of the pages out (512 requests of up to 8192 tokens leave and as many come, with their slot
+// map: 15.4 us; when the size was chosen 14.4 in blocks of 512 threads, 16.4 of 1024, 19.4 of 256,
+// and 25.4 in one block of 1024 threads).  The kernels here start while their
 // predecessor ends (programmatic launch) and wait for it before they touch memory.
 #include "paged.cuh"
 

@@ -13,7 +13,7 @@ namespace {
 // the only one whose older rows lie in the tail, so the CTA has them in registers before it
 // overwrites any.  A request that fills no block (most of a decode step) is one item per 16 heads,
 // a copy of its rows.  Bound by instructions (19 a value) and the two barriers of a key item: those
-// prompts' 105 MB in 34 us, 3.1 TB/s, 55.6 with the read-back.  Four CTAs an SM: 64.3 us with the
+// prompts' 105 MB in 35 us, 3.0 TB/s, 54.4 with the read-back.  Four CTAs an SM: 64.3 us with the
 // read-back before the last steps, three 69.9, five 65.4, six 66.8, and a CTA per item 68.8.
 // The division per word of eight codes with one near a half instead of per code: 63.7 for 58.6;
 // each thread's own reciprocals of its channels' scales instead of one per channel: 58.6 for 55.6.
