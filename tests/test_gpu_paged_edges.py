@@ -155,6 +155,68 @@ def test_slot_map_of_the_last_rows_that_offsets_can_name():
     assert pos[M - 14:].tolist() == [-7] * 3 + [3, 4] + list(range(40, 49))
 
 
+@pytest.mark.parametrize("batch,max_pages", [(100, 40), (700, 5)])
+def test_captured_requests_that_leave_and_come(batch, max_pages):
+    """Release, extend and slot map as clusters, captured once and replayed with other requests and counts."""
+    r = np.random.default_rng(batch)
+    pair = Pair(batch + 50, max_pages, batch * max_pages // 3, 1)
+    x, o, t = pair.c.index, pair.o, 64 * batch
+    gone, come, n = (torch.empty(b, dtype=torch.int32, device="cuda") for b in (batch // 2, batch, batch))
+    start, cu = (torch.empty(batch + e, dtype=torch.int32, device="cuda") for e in (0, 1))
+    place, pos = (torch.empty(t, dtype=torch.int32, device="cuda") for _ in range(2))
+    gone.fill_(-1), come.fill_(-1), n.zero_()
+
+    def step():
+        paged.fl_paged_release(x, gone)
+        paged.fl_paged_extend(x, come, n, start, cu)
+        paged.fl_paged_slot_map(x, come, start, cu, place, pos)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(6):
+        leave, enter = r.permutation(batch + 50)[: batch // 2], r.permutation(batch + 50)[:batch]
+        leave[r.random(len(leave)) < 0.1] = -1
+        new = r.integers(0, 128, batch)
+        new[-1] = max(0, t - int(new[:-1].sum())) if i == 3 else new[-1]
+        gone.copy_(i32(leave)), come.copy_(i32(enter)), n.copy_(i32(new))
+        place.fill_(-7), pos.fill_(-7)
+        graph.replay()
+        torch.cuda.synchronize()
+        o.release(leave, len(leave))
+        ostart, ocu = o.extend(enter, new)
+        assert start.tolist() == ostart.tolist() and cu.tolist() == ocu.tolist()
+        pair.same_index()
+        oplace, opos = o.slot_map(enter, ostart, ocu, t)
+        assert place.tolist() == oplace.tolist() and pos.tolist() == opos.tolist()
+    code, detail, count = pair.c.status()
+    assert count == len(o.errors) and (not count or (code, detail) in o.errors)
+
+
+def test_a_cache_whose_every_call_is_on_another_stream():
+    g = gen(14)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        pair = Pair(4, 40, 120, 2, 8)
+        for slots, n in (([2, 0, 3], [700, 1, 64 * 35]), ([0, 2, 1], [129, 1, 5]), ([3], [1])):
+            pair.step(slots, n, g)
+        q = bf16(g, 4, 8, D, scale=1.5)
+        lse = torch.empty(4, 8, device="cuda")
+        o = pair.c.attend(0, None, q.cuda(), lse=lse)
+        sel = pair.c.select(0, None, q.cuda(), 6)
+        place, _ = pair.c.places(i32([2]), i32([0]), i32([0, 701]), 701)
+        k, v = pair.c.read(0, place)
+        pair.same_bytes()
+        check_attention(pair, None, q, o, lse)
+        check_selection(pair, range(4), q, sel, 6)
+        for got, ref in zip((k, v), pair.o.keys_values(2, 1)):
+            assert torch.equal(got[:, 1].cpu(), torch.from_numpy(ref.astype(np.float32)).bfloat16())
+        pair.c.release(None)
+        assert pair.c.index.n_free.item() == 120 and pair.c.status()[2] == 0
+
+
 # ------------------------------------------------------------------------------- append and read
 def test_append_stops_at_offsets_that_descend():
     g = gen(2)
